@@ -431,6 +431,58 @@ kvd_status kvd_decode_step_e4m3(const void *q, void *k_cache, void *v_cache, con
                                 float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
                                 uint32_t *err_word, void *stream);
 
+/*
+ * kvd_rope_append / kvd_paged_rope_append -- the append of a step with the
+ * position rotation applied on the way (rotary position embedding), for models
+ * whose q and new keys arrive unrotated.  No counterpart in the source pages
+ * (their model adds learned positions to its input).
+ *
+ * For every sequence b < B and new token i < N, at position
+ *   p = pos_base + (positions != NULL ? positions[b * N + i] : past_len[b] + i)
+ * every row of q and k_new is rotated in its first rot_dim elements: with the
+ * angle a_f = p * inv_freq[f], f < rot_dim / 2, the pair (x, y) becomes
+ *   (x cos a_f - y sin a_f, x sin a_f + y cos a_f);
+ * a pair is elements (f, f + rot_dim / 2), or (2f, 2f + 1) when interleaved is
+ * not 0.  Elements rot_dim .. D-1 are copied.  Then
+ *   q_out[b, h, i, :]                = rotated q
+ *   k_cache[b, h, past_len[b]+i, :]  = rotated k_new   (page slots when paged)
+ *   v_cache[b, h, past_len[b]+i, :]  = v_new           (bit copy)
+ * and no other slot is touched.  Angles are exact whatever the position: the
+ * whole turns of p * inv_freq drop out in 64-bit integers.  The rotation is
+ * fp32, rounded once.
+ *
+ *   q, q_out          device, [B, H_q, N, D]; q_out dense; q_out may be q when q
+ *                     is dense too (any other overlap is an error of the caller)
+ *   k_new, v_new      device, [B, H_kv, N, D]
+ *   strides           host int64[9] or NULL (all dense): the element strides of
+ *                     q, k_new and v_new per sequence, head and token, each at
+ *                     least 0 and a multiple of 16 bytes (rows themselves are
+ *                     dense): the three parts of a fused projection's rows
+ *                     [B, N, (H_q + 2 H_kv) * D] are passed as they lie
+ *   positions         device int32[B, N] or NULL
+ *   inv_freq          device fp64[rot_dim / 2], finite, magnitudes below 2^60:
+ *                     radians per position
+ *   rot_dim           even, 2 .. D; a multiple of 32 bytes of elements
+ *                     (interleaved: 16 bytes), else KVD_ERR_UNSUPPORTED
+ *   D                 a multiple of 16 bytes of elements, at most 4096
+ * dtype (fp32, bf16 or fp16) covers rows, caches and q_out.  Other arguments,
+ * errors and device-side checks as for kvd_append and kvd_paged_append; a
+ * sequence skipped for its past_len has its q_out rows left unwritten too, and
+ * a token whose page is not in the pool has only its q_out rows written.
+ */
+kvd_status kvd_rope_append(const void *q, void *q_out, void *k_cache, void *v_cache, const void *k_new,
+                           const void *v_new, const int64_t *strides, const int32_t *past_len,
+                           const int32_t *positions, int pos_base, const double *inv_freq, int rot_dim,
+                           int interleaved, int B, int H_q, int H_kv, int T_max, int D, int N, int max_past_len,
+                           kvd_dtype dtype, uint32_t *err_word, void *stream);
+
+kvd_status kvd_paged_rope_append(const void *q, void *q_out, void *k_pages, void *v_pages, const void *k_new,
+                                 const void *v_new, const int64_t *strides, const int32_t *block_table,
+                                 const int32_t *past_len, const int32_t *positions, int pos_base,
+                                 const double *inv_freq, int rot_dim, int interleaved, int B, int H_q, int H_kv, int D,
+                                 int N, int page_size, int max_pages, int num_pages, int max_past_len, kvd_dtype dtype,
+                                 uint32_t *err_word, void *stream);
+
 /* kvd_workspace_init -- zero-fill a workspace on `stream` (asynchronous), as
  * kvd_decode_attention and kvd_decode_step need before a workspace's first use. */
 kvd_status kvd_workspace_init(void *workspace, size_t workspace_bytes, void *stream);

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "kvd_attention.cuh"
+#include "kvd_host.cuh"
 
 namespace kvd {
 
@@ -137,6 +138,31 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(const AppendE4m3Args a
         stg128(a.k_cache + dst, e4m3_chunk_from<T>(a.k_new + src, a.k_scale));
         stg128(a.v_cache + dst, e4m3_chunk_from<T>(a.v_new + src, a.v_scale));
     }
+}
+
+int elem_bytes(kvd_dtype dt)
+{
+    switch (dt) {
+    case KVD_F32: return 4;
+    case KVD_BF16:
+    case KVD_F16: return 2;
+    case KVD_E4M3: return 1;
+    default: return 0;
+    }
+}
+
+kvd_status check_paged(const PagedCache &pc, int *T_max, int *page_shift)
+{
+    if (pc.block_table == nullptr || pc.max_pages < 1 || pc.num_pages < 1) return KVD_ERR_INVALID_ARG;
+    if (pc.page_size < 64 || (pc.page_size & (pc.page_size - 1)) != 0 || pc.page_size > (1 << 24))
+        return KVD_ERR_INVALID_ARG;
+    const long long cap = (long long)pc.max_pages * pc.page_size;
+    if (cap > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
+    *T_max = (int)cap;
+    int sh = 0;
+    while ((1 << sh) < pc.page_size) ++sh;
+    *page_shift = sh;
+    return KVD_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -337,24 +363,9 @@ kvd_status cluster_fits(int dev, const void *fn, int threads, int smem, int c, b
     return KVD_OK;
 }
 
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 #ifdef KVD_TIMEOUT_TEST
 int g_test_stall = 0;  // test builds: plant kArgTestStall in the next launches
 #endif
-
-int elem_bytes(kvd_dtype dt)
-{
-    switch (dt) {
-    case KVD_F32: return 4;
-    case KVD_BF16:
-    case KVD_F16: return 2;
-    case KVD_E4M3: return 1;
-    default: return 0;
-    }
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The split-T plan of one decode_attention call.
 struct Plan {
@@ -538,6 +549,14 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
 }
 
 }  // namespace
+
+kvd_status current_sm_count(int *sms)
+{
+    int dev = 0;
+    const kvd_status st = current_device(&dev);
+    return st != KVD_OK ? st : sm_count(dev, sms);
+}
+
 }  // namespace kvd
 
 using namespace kvd;
@@ -618,32 +637,6 @@ kvd_status kvd_decode_plan(int B, int H_q, int H_kv, int D, int N, int max_past_
 
 }  // extern "C"
 
-namespace {
-
-// Attention (k_new == v_new == null) or the fused step (append inside).
-// A paged cache: block table and pool geometry (null table = contiguous cache).
-struct PagedCache {
-    const int32_t *block_table;
-    int page_size, max_pages, num_pages;
-};
-
-// Checks of the paged geometry; on success *T_max = max_pages * page_size.
-kvd_status check_paged(const PagedCache &pc, int *T_max, int *page_shift)
-{
-    if (pc.block_table == nullptr || pc.max_pages < 1 || pc.num_pages < 1) return KVD_ERR_INVALID_ARG;
-    if (pc.page_size < 64 || (pc.page_size & (pc.page_size - 1)) != 0 || pc.page_size > (1 << 24))
-        return KVD_ERR_INVALID_ARG;
-    const long long cap = (long long)pc.max_pages * pc.page_size;
-    if (cap > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
-    *T_max = (int)cap;
-    int sh = 0;
-    while ((1 << sh) < pc.page_size) ++sh;
-    *page_shift = sh;
-    return KVD_OK;
-}
-
-}  // namespace
-
 // Host checks of a kvd_decode_attention call (contiguous cache, no E4M3) and
 // the workspace it needs, without launching anything: the bytes, and the
 // region [*zero_off, *zero_off + *zero_bytes) that must be zero when the
@@ -676,6 +669,7 @@ kvd_status decode_attention_prepare(const void *q, const void *k_cache, const vo
 
 namespace {
 
+// Attention (k_new == v_new == null) or the fused step (append inside).
 kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
                          const void *v_new, void *out, const int32_t *past_len, int B, int H_q, int H_kv,
                          int T_max, int D, int N, int max_past_len, float scale, kvd_dtype dtype,

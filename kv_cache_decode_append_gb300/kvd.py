@@ -105,6 +105,10 @@ class _Lib:
         lib.kvd_decode_step_e4m3.restype = ci
         lib.kvd_decode_step_e4m3.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, cf, cf, cf,
                                              vp, sz, u32p, vp]
+        lib.kvd_rope_append.restype = ci
+        lib.kvd_rope_append.argtypes = [vp] * 9 + [ci, vp] + [ci] * 9 + [ci, u32p, vp]
+        lib.kvd_paged_rope_append.restype = ci
+        lib.kvd_paged_rope_append.argtypes = [vp] * 10 + [ci, vp] + [ci] * 11 + [ci, u32p, vp]
         lib.kvd_decode_attention_noalloc.restype = ci
         lib.kvd_decode_attention_noalloc.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, cf,
                                                      ci, u32p, vp]
@@ -564,6 +568,101 @@ def kvd_decode_step_e4m3(q, k_cache, v_cache, k_new, v_new, out, past_len, max_p
                                   N, int(max_past_len), float(scale), float(k_scale), float(v_scale), ws_ptr,
                                   ws_bytes, _ptr(err_word), _stream_handle(stream))
     _check("kvd_decode_step_e4m3", st)
+
+
+# ---------------------------------------------------------------------------------
+# rotated append
+def _same_device(*tensors) -> None:
+    """The tensors (None skipped) lie on one device, the current one: the library launches there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{dev}), got {t.device}")
+
+
+def _need_rows(name: str, t: torch.Tensor, dtype) -> None:
+    """[B, H, N, D] rows: each row contiguous, the rows at any non-negative strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
+        raise ValueError(f"{name} must be [B, H, N, D] with contiguous rows")
+
+
+def _rope_rows(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, pos_base, positions, err_word):
+    """Checks common to the rotated appends; returns (B, H_q, H_kv, N, D, strides or None)."""
+    dt = k_cache.dtype
+    for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
+        _need_rows(n, t, dt)
+    for n, t in (("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache)):
+        _need_cuda(n, t, dt)
+    _need_cuda("past_len", past_len, torch.int32)
+    _need_cuda("inv_freq", inv_freq, torch.float64)
+    B, H_q, N, D = q.shape
+    H_kv = k_new.shape[1]
+    if positions is not None:
+        _need_cuda("positions", positions, torch.int32)
+        if tuple(positions.shape) != (B, N):
+            raise ValueError("positions must be [B, N]")
+    if err_word is not None:
+        _need_cuda("err_word", err_word, torch.int32)
+    if tuple(k_new.shape) != (B, H_kv, N, D) or v_new.shape != k_new.shape or q_out.shape != q.shape:
+        raise ValueError("shape mismatch between q, q_out and the new K/V")
+    if v_cache.shape != k_cache.shape or k_cache.dim() != 4 or k_cache.shape[1] != H_kv or k_cache.shape[3] != D:
+        raise ValueError("shape mismatch between the caches and the new K/V")
+    if past_len.numel() != B:
+        raise ValueError("past_len must hold B entries")
+    _same_device(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, positions, err_word)
+    if not -(1 << 31) <= pos_base < 1 << 31:
+        raise ValueError("pos_base must fit in 32 bits")
+    if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        raise ValueError("q_out may be q only when q is contiguous")
+    if q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous():
+        return B, H_q, H_kv, N, D, None
+    # (a dimension of one row has no stride that matters; torch may report any)
+    st = [s if n > 1 else 0 for t in (q, k_new, v_new) for s, n in zip(t.stride()[:3], t.shape[:3])]
+    return B, H_q, H_kv, N, D, (ctypes.c_int64 * 9)(*st)
+
+
+def kvd_rope_append(q, q_out, k_cache, v_cache, k_new, v_new, past_len, max_past_len: int, inv_freq,
+                    interleaved: bool = False, pos_base: int = 0, positions=None, err_word=None,
+                    stream=None) -> None:
+    """kvd_append with the position rotation on the way: rotated ``q`` into ``q_out`` [B,H_q,N,D],
+    rotated ``k_new`` and plain ``v_new`` [B,H_kv,N,D] into slots ``past_len[b] + i``.
+
+    ``inv_freq`` fp64 [rot_dim / 2]: radians per position; the first ``rot_dim`` elements of a row are
+    rotated, in pairs (f, f + rot_dim / 2), or (2f, 2f + 1) when ``interleaved``.  A token's position
+    is ``pos_base + positions[b, i]``, without ``positions`` ``pos_base + past_len[b] + i``.  ``q``,
+    ``k_new`` and ``v_new`` may be strided views with contiguous rows (the parts of a fused
+    projection); ``q_out`` may be ``q``."""
+    B, H_q, H_kv, N, D, strides = _rope_rows(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, pos_base,
+                                             positions, err_word)
+    if k_cache.shape[0] != B:
+        raise ValueError("shape mismatch between the caches and the new K/V")
+    st = raw.kvd_rope_append(q.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
+                             v_new.data_ptr(), strides, past_len.data_ptr(), _ptr(positions), int(pos_base),
+                             inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), B, H_q, H_kv,
+                             k_cache.shape[2], D, N, int(max_past_len), _dtype_code(k_cache), _ptr(err_word),
+                             _stream_handle(stream))
+    _check("kvd_rope_append", st)
+
+
+def kvd_paged_rope_append(q, q_out, k_pages, v_pages, k_new, v_new, block_table, past_len, max_past_len: int, inv_freq,
+                          interleaved: bool = False, pos_base: int = 0, positions=None, err_word=None,
+                          stream=None) -> None:
+    """kvd_rope_append into the page slots of tokens ``past_len[b] + i``."""
+    B, H_q, H_kv, N, D, strides = _rope_rows(q, q_out, k_new, v_new, k_pages, v_pages, past_len, inv_freq, pos_base,
+                                             positions, err_word)
+    num_pages, _, page_size, _, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
+    _same_device(block_table)
+    st = raw.kvd_paged_rope_append(q.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                   k_new.data_ptr(), v_new.data_ptr(), strides, block_table.data_ptr(),
+                                   past_len.data_ptr(), _ptr(positions), int(pos_base), inv_freq.data_ptr(),
+                                   2 * inv_freq.numel(), int(interleaved), B, H_q, H_kv, D, N, page_size, max_pages,
+                                   num_pages, int(max_past_len), _dtype_code(k_pages), _ptr(err_word),
+                                   _stream_handle(stream))
+    _check("kvd_paged_rope_append", st)
 
 
 def kvd_decode_attention_noalloc(q, k_cache, v_cache, out, past_len, max_past_len: int,

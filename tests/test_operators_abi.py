@@ -1,0 +1,70 @@
+"""Host-side refusals of the rotated append, scored attention and shared-prefix
+attention: documented statuses before anything touches a GPU.  CPU only."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kv_cache_decode_append_gb300 import build as kbuild
+    from kv_cache_decode_append_gb300 import kvd
+    kbuild.build()
+    return kvd.load()
+
+
+# A fake, 256-byte aligned address: every call below is refused on the host
+# before any pointer is dereferenced or any CUDA call is made.
+A = 1 << 20
+OK, INVALID, CAPACITY, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3, 4
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
+
+
+def _rope(lib, q=A, q_out=A, k=A, v=A, kn=A, vn=A, strides=None, past=A, positions=None, freq=A, rot=64, pairs=0, B=1,
+          H_q=4, H_kv=2, T_max=64, D=64, N=1, max_past=10, dtype=BF16):
+    return lib.kvd_rope_append(q, q_out, k, v, kn, vn, strides, past, positions, 0, freq, rot, pairs, B, H_q, H_kv,
+                               T_max, D, N, max_past, dtype, None, None)
+
+
+def _paged_rope(lib, q=A, q_out=A, k=A, v=A, kn=A, vn=A, strides=None, table=A, past=A, positions=None, freq=A, rot=64,
+                pairs=0, B=1, H_q=4, H_kv=2, D=64, N=1, page_size=64, max_pages=1, num_pages=8, max_past=10,
+                dtype=BF16):
+    return lib.kvd_paged_rope_append(q, q_out, k, v, kn, vn, strides, table, past, positions, 0, freq, rot, pairs, B,
+                                     H_q, H_kv, D, N, page_size, max_pages, num_pages, max_past, dtype, None, None)
+
+
+@pytest.mark.parametrize("call", [_rope, _paged_rope])
+def test_rope_append_refusals(lib, call):
+    for name in ("q", "q_out", "k", "v", "kn", "vn", "past", "freq"):
+        assert call(lib, **{name: None}) == INVALID, name
+    for name in ("q", "q_out", "k", "v", "kn", "vn"):
+        assert call(lib, **{name: A + 8}) == INVALID, name
+    assert call(lib, freq=A + 4) == INVALID
+    assert call(lib, B=-1) == INVALID
+    assert call(lib, H_q=0) == INVALID
+    assert call(lib, N=0) == INVALID
+    assert call(lib, max_past=-1) == INVALID
+    assert call(lib, rot=0) == INVALID
+    assert call(lib, rot=33) == INVALID
+    assert call(lib, rot=66) == INVALID           # more than the row
+    assert call(lib, rot=24) == UNSUPPORTED       # halves of 12: not whole 16-byte chunks
+    assert call(lib, rot=20, pairs=1) == UNSUPPORTED
+    assert call(lib, rot=24, pairs=1, B=0) == OK
+    assert call(lib, D=68) == UNSUPPORTED
+    assert call(lib, D=8192) == UNSUPPORTED
+    assert call(lib, dtype=E4M3) == UNSUPPORTED
+    assert call(lib, dtype=9) == UNSUPPORTED
+    assert call(lib, max_past=60, N=5) == CAPACITY
+    assert call(lib, max_past=(1 << 31) - 1) == CAPACITY
+    assert call(lib, strides=(ctypes.c_int64 * 9)(256, 64, 64, 128, 64, 64, 128, -64, 64)) == INVALID
+    assert call(lib, strides=(ctypes.c_int64 * 9)(256, 64, 60, 128, 64, 64, 128, 64, 64)) == INVALID
+    assert call(lib, B=0) == OK
+
+
+def test_paged_rope_append_geometry(lib):
+    assert _paged_rope(lib, table=None) == INVALID
+    assert _paged_rope(lib, page_size=48) == INVALID
+    assert _paged_rope(lib, page_size=32) == INVALID
+    assert _paged_rope(lib, max_pages=0) == INVALID
+    assert _paged_rope(lib, num_pages=0) == INVALID
+    assert _paged_rope(lib, max_pages=1 << 26) == INVALID

@@ -483,6 +483,62 @@ kvd_status kvd_paged_rope_append(const void *q, void *q_out, void *k_pages, void
                                  int N, int page_size, int max_pages, int num_pages, int max_past_len, kvd_dtype dtype,
                                  uint32_t *err_word, void *stream);
 
+/*
+ * kvd_decode_attention_scored / kvd_paged_decode_attention_scored --
+ * kvd_decode_attention (kvd_paged_decode_attention) with modified scores: a cap,
+ * a penalty on the distance, a sliding window, a prefix that every row sees,
+ * documents packed into a sequence, in any combination.  No counterpart in the
+ * source pages (their model masks causally and adds nothing to its scores).
+ *
+ * For sequence b, query head hq, new row i at position p = past_len[b] + i, and
+ * key j of 0 .. past_len[b] + N - 1 (s_j = scale * q . k_j as in
+ * kvd_decode_attention):
+ *   y_j = (softcap > 0 ? softcap * tanh(s_j / softcap) : s_j)
+ *         - (slopes != NULL ? slopes[hq] * |p - j| : 0)
+ *   row i sees j  <=>  j >= doc  and  (j < prefix  or  p - window < j <= p)
+ *   out[b,hq,i,:] = sum over seen j of softmax(y)_j * v_j; zeros if it sees none
+ * with window = infinity when 0, prefix = prefix_len[b] (0 when NULL) and doc =
+ * max(doc_start[b,0], doc_start[b,i]) (0 when NULL): documents lie in order, so
+ * no row's document begins before the first row's.
+ *
+ * Tiles of keys that no row of a sequence sees are not read, and their
+ * block-table entries not looked up, so a windowed layer may have freed those
+ * pages; keys that no row sees may hold anything, NaN included.  (A NaN or
+ * infinity in a key or value that only some of the sequence's rows see may reach
+ * the others.)
+ *
+ *   score       host struct, read during the call; its pointers are device
+ *               memory, 4-byte aligned, used like past_len
+ *   workspace   of at least kvd_decode_scored_workspace_bytes(...) bytes,
+ *               otherwise as for kvd_decode_attention
+ * fp32, bf16 and fp16; other arguments, limits, errors and device-side checks as
+ * for the plain calls.  softcap negative, infinite or NaN, or window negative:
+ * KVD_ERR_INVALID_ARG.  16-bit dtypes take tanh as 1 - 2 / (1 + e^2x) with
+ * approximate exponential and reciprocal (off by about 2^-21 softcap).
+ */
+typedef struct kvd_score {
+    float softcap;             /* > 0: scores capped at +- softcap; 0: not */
+    const float *slopes;       /* device fp32[H_q] or NULL: penalty per key of distance */
+    int window;                /* > 0: a row sees the last `window` keys up to its own; 0: all */
+    const int32_t *doc_start;  /* device int32[B, N] or NULL: first key of the row's document */
+    const int32_t *prefix_len; /* device int32[B] or NULL: the first keys, seen by every row */
+} kvd_score;
+
+size_t kvd_decode_scored_workspace_bytes(int B, int H_q, int H_kv, int D, int N, int max_past_len,
+                                         kvd_dtype dtype);
+
+kvd_status kvd_decode_attention_scored(const void *q, const void *k_cache, const void *v_cache, void *out,
+                                       const int32_t *past_len, const kvd_score *score, int B, int H_q, int H_kv,
+                                       int T_max, int D, int N, int max_past_len, float scale, kvd_dtype dtype,
+                                       void *workspace, size_t workspace_bytes, uint32_t *err_word, void *stream);
+
+kvd_status kvd_paged_decode_attention_scored(const void *q, const void *k_pages, const void *v_pages, void *out,
+                                             const int32_t *block_table, const int32_t *past_len,
+                                             const kvd_score *score, int B, int H_q, int H_kv, int D, int N,
+                                             int page_size, int max_pages, int num_pages, int max_past_len,
+                                             float scale, kvd_dtype dtype, void *workspace, size_t workspace_bytes,
+                                             uint32_t *err_word, void *stream);
+
 /* kvd_workspace_init -- zero-fill a workspace on `stream` (asynchronous), as
  * kvd_decode_attention and kvd_decode_step need before a workspace's first use. */
 kvd_status kvd_workspace_init(void *workspace, size_t workspace_bytes, void *stream);

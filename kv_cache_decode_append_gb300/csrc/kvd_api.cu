@@ -181,7 +181,7 @@ struct OccEntry {
     int smem;
     int ctas_per_sm;
 };
-OccEntry g_occ[256];
+OccEntry g_occ[512];
 int g_occ_n = 0;
 
 constexpr int kMaxSmemPerCta = 227 * 1024;
@@ -314,7 +314,7 @@ kvd_status occupancy(int dev, const void *fn, int threads, int smem, int *ctas_p
     int occ = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem) != cudaSuccess || occ <= 0)
         return KVD_ERR_CUDA;
-    if (g_occ_n < 256) g_occ[g_occ_n++] = OccEntry{dev, fn, smem, occ};
+    if (g_occ_n < 512) g_occ[g_occ_n++] = OccEntry{dev, fn, smem, occ};
     *ctas_per_sm = occ;
     return KVD_OK;
 }
@@ -327,7 +327,7 @@ struct ClusterEntry {
     int smem, c;
     bool ok;
 };
-ClusterEntry g_cl[64];
+ClusterEntry g_cl[128];
 int g_cl_n = 0;
 
 kvd_status cluster_fits(int dev, const void *fn, int threads, int smem, int c, bool *ok)
@@ -358,7 +358,7 @@ kvd_status cluster_fits(int dev, const void *fn, int threads, int smem, int c, b
         (void)cudaGetLastError();
         n = 0;
     }
-    if (g_cl_n < 64) g_cl[g_cl_n++] = ClusterEntry{dev, fn, smem, c, n > 0};
+    if (g_cl_n < 128) g_cl[g_cl_n++] = ClusterEntry{dev, fn, smem, c, n > 0};
     *ok = n > 0;
     return KVD_OK;
 }
@@ -418,6 +418,7 @@ kvd_status min_occupancy(int dev, const AttnVariant &vp, const AttnVariant &vt, 
 {
     *occ = 1 << 30;
     for (const void *fn : {vp.fn, vp.fused_fn, vt.fn, vt.fused_fn}) {
+        if (fn == nullptr) continue;  // (modified scores: attention only)
         int o = 0;
         const kvd_status st = occupancy(dev, fn, vp.threads, smem, &o);
         if (st != KVD_OK) return st;
@@ -426,8 +427,21 @@ kvd_status min_occupancy(int dev, const AttnVariant &vp, const AttnVariant &vt, 
     return KVD_OK;
 }
 
+// The two builds with modified scores, by row block (16: mma.sync, 128: tcgen05).
+bool pick_scored_builds(kvd_dtype dtype, int D, int rb, bool paged, AttnVariant *vp, AttnVariant *vt)
+{
+    switch (dtype) {
+    case KVD_F32: return attn_variant_scored_f32(D, rb, paged, vp) && attn_variant_scored_f32_tk(D, rb, paged, vt);
+    case KVD_BF16: return attn_variant_scored_bf16(D, rb, paged, vp) && attn_variant_scored_bf16_tk(D, rb, paged, vt);
+    case KVD_F16: return attn_variant_scored_f16(D, rb, paged, vp) && attn_variant_scored_f16_tk(D, rb, paged, vt);
+    default: return false;
+    }
+}
+
+// scored: the kernels with modified scores.  keys: an upper bound on the keys
+// a sequence's rows see together (0: max_past_len + N).
 kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype,
-                     Plan *pl, bool paged = false)
+                     Plan *pl, bool paged = false, bool scored = false, long long keys = 0)
 {
     kvd_status st = check_shapes(B, H_q, H_kv, D, N, max_past_len, dtype);
     if (st != KVD_OK) return st;
@@ -444,7 +458,10 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     pl->rb = pl->tc5 ? 128 : pl->mma ? 16 : pl->rows <= 1 ? 1 : pl->rows <= 2 ? 2 : (pl->rows <= 4 || dtype == KVD_E4M3) ? 4 : 8;
     pl->n_rowblocks = (pl->rows + pl->rb - 1) / pl->rb;
     AttnVariant vp, vt, op, ot;  // this layout's builds, and the other layout's
-    if (pl->tc5) {
+    if (scored) {
+        if (!pick_scored_builds(dtype, D, pl->rb, paged, &vp, &vt) || !pick_scored_builds(dtype, D, pl->rb, !paged, &op, &ot))
+            return KVD_ERR_UNSUPPORTED;
+    } else if (pl->tc5) {
         const auto builds = [&](bool pg, AttnVariant *p, AttnVariant *t) {
             return dtype == KVD_BF16 ? attn_variant_tc5_bf16(D, pg, p) && attn_variant_tc5_bf16_tk(D, pg, t)
                                      : attn_variant_tc5_f16(D, pg, p) && attn_variant_tc5_f16_tk(D, pg, t);
@@ -473,8 +490,9 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     pl->v = vp;
 
     // Shared memory holds the ring plus two per-sequence tables (B + 1 tile
-    // prefix sums, B history lengths).
-    const size_t smem = (size_t)pl->v.fixed_smem_bytes + (((size_t)2 * B + 1) * 4 + 15) / 16 * 16;
+    // prefix sums, B history lengths); with modified scores two more (first
+    // document key, prefix length).
+    const size_t smem = (size_t)pl->v.fixed_smem_bytes + (((size_t)(scored ? 4 : 2) * B + 1) * 4 + 15) / 16 * 16;
     if (smem > (size_t)kMaxSmemPerCta) return KVD_ERR_UNSUPPORTED;
     pl->smem = (int)smem;
 
@@ -491,11 +509,10 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
 
     // One CTA per resident slot; each takes an equal share of all tiles.
     // Small layers leave room on every SM for the calls that follow.
-    const long long kv_bytes_hint =
-        2LL * B * H_kv * ((long long)max_past_len + N) * D * elem_bytes(dtype);
+    const long long t_hint = keys > 0 ? keys : (long long)max_past_len + N;
+    const long long kv_bytes_hint = 2LL * B * H_kv * t_hint * D * elem_bytes(dtype);
     pl->early = !pl->mma && !pl->tc5 && kv_bytes_hint <= kEarlyMaxBytes;
     pl->grid = sms * (pl->early && occ > kEarlyCtasPerSm ? kEarlyCtasPerSm : occ);
-    const long long t_hint = (long long)max_past_len + N;
     pl->max_tiles = (int)((t_hint + pl->v.tile_keys - 1) / pl->v.tile_keys);
     // Heads split across CTAs: merged inside the kernel by the CTA that
     // finishes a head last, unless the ranges are long (at most
@@ -520,10 +537,10 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
             if ((st = cluster_fits(dev, pl->v.cluster_fn, pl->v.threads, (int)smem_cl, c, &fits)) != KVD_OK)
                 return st;
             bool fits2 = false;
-            if (fits &&
+            if (fits && pl->v.cluster_fused_fn != nullptr &&
                 (st = cluster_fits(dev, pl->v.cluster_fused_fn, pl->v.threads, (int)smem_cl, c, &fits2)) != KVD_OK)
                 return st;
-            fits = fits && fits2;
+            fits = fits && (fits2 || pl->v.cluster_fused_fn == nullptr);
         }
         if (fits) {
             pl->cluster = c;
@@ -669,13 +686,23 @@ kvd_status decode_attention_prepare(const void *q, const void *k_cache, const vo
 
 namespace {
 
+// The most keys that a sequence's rows see together: with a window and no
+// prefix, the window of its first row to its last row, in whole tiles (any
+// variant's tiles: 64 keys at most).
+long long score_keys_bound(const kvd_score &s, int N, int max_past_len)
+{
+    const long long all = (long long)max_past_len + N;
+    if (s.window == 0 || s.prefix_len != nullptr) return all;
+    return std::min<long long>(all, (long long)s.window + N - 1 + 64);
+}
+
 // Attention (k_new == v_new == null) or the fused step (append inside).
 kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache, const void *k_new,
                          const void *v_new, void *out, const int32_t *past_len, int B, int H_q, int H_kv,
                          int T_max, int D, int N, int max_past_len, float scale, kvd_dtype dtype,
                          void *workspace, size_t workspace_bytes, uint32_t *err_word, void *stream,
                          const PagedCache *paged = nullptr, const float *e4m3_scales = nullptr,
-                         uint32_t step_flags = 0u)
+                         uint32_t step_flags = 0u, const kvd_score *score = nullptr)
 {
     if (!q || !k_cache || !v_cache || !out || !past_len) return KVD_ERR_INVALID_ARG;
     kvd_status st = check_shapes(B, H_q, H_kv, D, N, max_past_len, dtype);
@@ -691,16 +718,24 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
         return KVD_ERR_INVALID_ARG;
     if ((long long)max_past_len + N > T_max) return KVD_ERR_CAPACITY;
+    long long keys = 0;
+    if (score != nullptr) {
+        if (!(score->softcap >= 0.f && score->softcap < INFINITY) || score->window < 0) return KVD_ERR_INVALID_ARG;
+        for (const void *p : {(const void *)score->slopes, (const void *)score->doc_start, (const void *)score->prefix_len})
+            if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return KVD_ERR_INVALID_ARG;
+        keys = score_keys_bound(*score, N, max_past_len);
+    }
     if (B == 0) return KVD_OK;
 
     Plan pl;
-    if ((st = make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, paged != nullptr)) != KVD_OK) return st;
+    if ((st = make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, paged != nullptr, score != nullptr, keys)) != KVD_OK)
+        return st;
     if (workspace == nullptr || workspace_bytes < pl.ws_bytes ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return KVD_ERR_WORKSPACE;
 
     char *ws = static_cast<char *>(workspace);
-    AttnArgs a;
+    AttnScoredArgs a;  // (the kernels without modified scores take its AttnArgs part)
     a.q = q;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
@@ -737,6 +772,15 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
     const float sc = (scale > 0.f) ? scale : 1.0f / sqrtf((float)D);
     // (E4M3: key = k_scale x stored code, folded into the q pre-scale)
     a.qscale = sc * kLog2e * (e4m3_scales != nullptr ? e4m3_scales[0] : 1.0f);
+
+    if (score != nullptr) {
+        a.slopes = score->slopes;
+        a.doc_start = score->doc_start;
+        a.prefix_len = score->prefix_len;
+        a.cap = score->softcap * kLog2e;
+        a.cap_in = score->softcap > 0.f ? 2.f / score->softcap : 0.f;  // (2 log2(e) / C)
+        a.window = score->window;
+    }
 
     // Both kernels are programmatic dependents of whatever precedes them on
     // the stream: they start early and wait (griddepcontrol.wait) before
@@ -917,6 +961,39 @@ kvd_status kvd_paged_decode_step(const void *q, void *k_pages, void *v_pages, co
     const PagedCache pc{block_table, page_size, max_pages, num_pages};
     return decode_launch(q, k_pages, v_pages, k_new, v_new, out, past_len, B, H_q, H_kv, 0, D, N,
                          max_past_len, scale, dtype, workspace, workspace_bytes, err_word, stream, &pc);
+}
+
+size_t kvd_decode_scored_workspace_bytes(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype)
+{
+    if (dtype == KVD_E4M3) return 0;
+    Plan pl;
+    if (make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, false, true) != KVD_OK) return 0;
+    return pl.ws_bytes;
+}
+
+kvd_status kvd_decode_attention_scored(const void *q, const void *k_cache, const void *v_cache, void *out,
+                                       const int32_t *past_len, const kvd_score *score, int B, int H_q, int H_kv,
+                                       int T_max, int D, int N, int max_past_len, float scale, kvd_dtype dtype,
+                                       void *workspace, size_t workspace_bytes, uint32_t *err_word, void *stream)
+{
+    if (score == nullptr) return KVD_ERR_INVALID_ARG;
+    return decode_launch(q, k_cache, v_cache, nullptr, nullptr, out, past_len, B, H_q, H_kv, T_max, D, N,
+                         max_past_len, scale, dtype, workspace, workspace_bytes, err_word, stream, nullptr, nullptr, 0u,
+                         score);
+}
+
+kvd_status kvd_paged_decode_attention_scored(const void *q, const void *k_pages, const void *v_pages, void *out,
+                                             const int32_t *block_table, const int32_t *past_len,
+                                             const kvd_score *score, int B, int H_q, int H_kv, int D, int N,
+                                             int page_size, int max_pages, int num_pages, int max_past_len,
+                                             float scale, kvd_dtype dtype, void *workspace, size_t workspace_bytes,
+                                             uint32_t *err_word, void *stream)
+{
+    if (score == nullptr) return KVD_ERR_INVALID_ARG;
+    const PagedCache pc{block_table, page_size, max_pages, num_pages};
+    return decode_launch(q, k_pages, v_pages, nullptr, nullptr, out, past_len, B, H_q, H_kv, 0, D, N,
+                         max_past_len, scale, dtype, workspace, workspace_bytes, err_word, stream, &pc, nullptr, 0u,
+                         score);
 }
 
 kvd_status kvd_append_e4m3(void *k_cache, void *v_cache, const void *k_new, const void *v_new,

@@ -120,6 +120,162 @@ enum FillMode {
 };
 static_assert(sizeof(AttnArgs) == 128, "keep the kernel parameter block at 128 bytes");
 
+// ---- modified scores (the kernels' kMod builds) ----
+//
+// A row of position p = P + i scores key j as
+//   y = log2(e) (cap tanh(s / cap) - slope |p - j|),  s = scale q . k_j
+// (without a cap: s itself) and sees it when
+//   j >= doc  and  (j < pre  or  p - window < j <= p).
+// Everything is in log2 units, as the unmodified scores: with
+// C = cap log2(e) and y0 = s log2(e), cap tanh(s / cap) log2(e) = C tanh(y0 / C).
+struct AttnScoredArgs : AttnArgs {
+    const float *slopes;        // [H_q] or null
+    const int32_t *doc_start;   // [B, N] or null
+    const int32_t *prefix_len;  // [B] or null
+    float cap;                  // C, or 0: no cap
+    float cap_in;               // 2 log2(e) / C
+    int window;                 // 0: none
+};
+template <bool kMod> using AttnArgsOf = typename std::conditional<kMod, AttnScoredArgs, AttnArgs>::type;
+
+// What one query row sees and how its scores are penalised.
+struct RowScore {
+    int p, lo, doc;  // position; first key of its window; first key of its document
+    float slope;     // log2(e) slope
+};
+
+// Whether the row sees all of the kTK keys from k0 on; whether it sees key.
+template <int kTK> __device__ __forceinline__ bool row_sees_all(const RowScore &r, int pre, int k0)
+{
+    return k0 >= r.doc && (k0 + kTK <= pre || (k0 >= r.lo && k0 + kTK <= r.p + 1));
+}
+__device__ __forceinline__ bool row_sees(const RowScore &r, int pre, int key)
+{
+    return key >= r.doc && (key < pre || (key >= r.lo && key <= r.p));
+}
+
+// C tanh(y0 / C).  For 16-bit results tanh z = 1 - 2 / (1 + e^2z) with the
+// approximate exp2 and reciprocal: off by at most about 2^-21 absolutely, which
+// moves a weight by C 2^-21 relatively (cap 50: 3e-5, a hundredth of a bf16
+// rounding).  fp32 results take tanhf.
+template <bool kExact> __device__ __forceinline__ float cap_score(float y0, float C, float cap_in)
+{
+    if constexpr (kExact) {
+        return C * tanhf(y0 / C);
+    } else {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(y0 * cap_in)));
+        return fmaf(-2.f * C, r, C);
+    }
+}
+
+// The tiles of one sequence: n_a tiles from a0 on (the prefix that every row
+// sees), then the rest up to n_tiles from b0 on (the rows' windows).  Tiles that
+// no row sees are not walked (nor their pages looked up); at least one tile is,
+// so that a sequence whose rows see nothing still gets its zero output.
+struct TileRegions {
+    int a0, n_a, b0, n_tiles;
+    int lo;  // first key of the first row's window (no later row looks further back)
+    __device__ __forceinline__ int tile(int k) const { return k < n_a ? a0 + k : b0 + (k - n_a); }
+};
+
+// First key of a sequence's documents and length of its all-seen prefix, as
+// the tile walk uses them: both within 0 .. P + N.
+__device__ __forceinline__ int2 seq_bounds(const AttnScoredArgs &a, int b, int P)
+{
+    const int T = P + a.N;
+    const int doc = a.doc_start != nullptr ? __ldg(a.doc_start + (size_t)b * a.N) : 0;
+    const int pre = a.prefix_len != nullptr ? __ldg(a.prefix_len + b) : 0;
+    return make_int2(min(max(doc, 0), T), min(max(pre, 0), T));
+}
+
+template <int kTK>
+__device__ __forceinline__ TileRegions tile_regions(int P, int N, int window, int doc, int pre)
+{
+    TileRegions g;
+    const int T = P + N;
+    g.lo = window > 0 ? max(0, P - window + 1) : 0;
+    const int n_end = (T + kTK - 1) / kTK;
+    g.b0 = min(max(doc, g.lo), T - 1) / kTK;
+    g.a0 = g.b0;
+    g.n_a = 0;
+    if (pre > doc) {
+        g.a0 = doc / kTK;
+        g.n_a = (pre + kTK - 1) / kTK - g.a0;
+        if (g.a0 + g.n_a >= g.b0) {  // (no gap)
+            g.b0 = min(g.a0, g.b0);
+            g.a0 = g.b0;
+            g.n_a = 0;
+        }
+    }
+    g.n_tiles = g.n_a + n_end - g.b0;
+    return g;
+}
+
+// What the tiles of a piece need of its sequence: the call's arguments, this
+// thread's rows, the sequence's bounds (seq_bounds; lo as TileRegions) and its
+// rows' documents (null: none).
+struct ModTile {
+    const AttnScoredArgs *sa;
+    const RowScore *rs;
+    const int32_t *docs;
+    int doc, pre, lo, P;
+};
+__device__ __forceinline__ ModTile mod_tile(const AttnScoredArgs &a, const RowScore *rs, int b, int P)
+{
+    const int2 db = seq_bounds(a, b, P);
+    return ModTile{&a, rs, a.doc_start != nullptr ? a.doc_start + (size_t)b * a.N : nullptr, db.x, db.y,
+                   a.window > 0 ? max(0, P - a.window + 1) : 0, P};
+}
+
+// A key of a walked tile that no row of the sequence sees: its value row may
+// hold anything (a freed slot, a padding token's row, NaN) and is replaced by
+// zeros.  The first row sees every cached key from doc and lo on, and each
+// new key is seen by its own row, unless that row's document begins later;
+// then the others are asked.
+__device__ __forceinline__ bool key_unseen(const ModTile &m, int key, int k_end)
+{
+    if (key >= k_end || key < m.doc || (key >= m.pre && key < m.lo)) return true;
+    if (m.docs == nullptr || key < m.P) return false;
+    const int d0 = __ldg(m.docs), window = m.sa->window;
+    for (int i = key < m.pre ? 0 : key - m.P; i < m.sa->N; ++i)
+        if (key >= max(d0, __ldg(m.docs + i)) && (key < m.pre || window == 0 || key > m.P + i - window)) return false;
+    return true;
+}
+
+// Whether a run of n keys from k0 on may hold such keys.
+__device__ __forceinline__ bool some_unseen(const ModTile &m, int k0, int n, int k_end)
+{
+    return k0 + n > k_end || k0 < m.doc || (k0 + n > m.pre && k0 < m.lo) || (m.docs != nullptr && k0 + n > m.P);
+}
+
+// A row of a piece's block: query row rg of KV head h of sequence b (rg past
+// the block's rows: the padding takes the last row's bounds and no penalty).
+__device__ __forceinline__ RowScore row_score(const AttnScoredArgs &a, int b, int h, int rg, int P)
+{
+    RowScore r;
+    const int i = rg % a.N;
+    r.p = P + i;
+    r.lo = a.window > 0 ? r.p - a.window + 1 : 0;
+    r.doc = 0;
+    if (a.doc_start != nullptr) {  // (a document never begins before the first row's)
+        const int32_t *d = a.doc_start + (size_t)b * a.N;
+        r.doc = max(__ldg(d), __ldg(d + i));
+    }
+    r.slope = a.slopes != nullptr && rg < a.rows ? __ldg(a.slopes + h * (a.rows / a.N) + rg / a.N) * kLog2e : 0.f;
+    return r;
+}
+
+// out = num / den; a row that sees no key gets 0 (kMod builds only: every
+// other row sees at least its own key).
+template <bool kMod> __device__ __forceinline__ float quotient(float num, float den)
+{
+    if constexpr (kMod)
+        return den == 0.f ? 0.f : num / den;
+    else
+        return num / den;
+}
+
 
 // Compile-time shape of one kernel variant: q / out elements T, cache
 // elements C (T, or E4M3 codes with bf16 q).
@@ -206,14 +362,16 @@ constexpr int kMetaSkip = 8;   // a speculative tile that turned out not to be n
 // rows when kTileRel (paged cache: kc is the slot of the tile's first key).
 // With an E4M3 cache (C != T) the new rows are quantized on the way in
 // (kv_scale: the K and V scales), exactly as the E4M3 append stores them.
-template <typename T, int D, int RB, bool kMasked, bool kFused, bool kTileRel = false, typename C = T>
+// kMod: the scores are modified and the rows' own bounds apply (mod) instead of lim.
+template <typename T, int D, int RB, bool kMasked, bool kFused, bool kTileRel = false, typename C = T, bool kMod = false>
 __device__ __forceinline__ void attn_tile(const unsigned char *Ks, const unsigned char *Vs,
                                           const f32x2 (&qv)[RB][AttnShape<T, D, RB, C>::kE / 2],
                                           f32x2 (&o)[RB][AttnShape<T, D, RB, C>::kE / 2], float (&m_run)[RB],
                                           float (&l_run)[RB], int warp, int grp, int j,
                                           int tile_k0, const int (&lim)[RB], int k_end, int P,
                                           const unsigned char *kn, const unsigned char *vn,
-                                          unsigned char *kc, unsigned char *vc, float2 kv_scale = float2{})
+                                          unsigned char *kc, unsigned char *vc, float2 kv_scale = float2{},
+                                          ModTile mod = ModTile{})
 {
     using S = AttnShape<T, D, RB, C>;
     using Ty = Elem<C>;
@@ -274,7 +432,25 @@ __device__ __forceinline__ void attn_tile(const unsigned char *Ks, const unsigne
 #pragma unroll
             for (int r = 0; r < RB; ++r) sc[u][r] += __shfl_xor_sync(0xffffffffu, sc[u][r], off);
     }
-    if constexpr (kMasked) {
+    if constexpr (kMod) {
+        constexpr bool kExact = sizeof(T) == 4;
+        if (mod.sa->cap > 0.f) {
+#pragma unroll
+            for (int u = 0; u < S::kKpg; ++u)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) sc[u][r] = cap_score<kExact>(sc[u][r], mod.sa->cap, mod.sa->cap_in);
+        }
+#pragma unroll
+        for (int u = 0; u < S::kKpg; ++u) {
+            const int key = tile_k0 + warp * S::kKpw + u * S::kGpw + grp;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                sc[u][r] = fmaf(-mod.rs[r].slope, fabsf((float)(mod.rs[r].p - key)), sc[u][r]);
+                if constexpr (kMasked)
+                    if (key >= k_end || !row_sees(mod.rs[r], mod.pre, key)) sc[u][r] = kNegInf;
+            }
+        }
+    } else if constexpr (kMasked) {
 #pragma unroll
         for (int u = 0; u < S::kKpg; ++u) {
             const int key = tile_k0 + warp * S::kKpw + u * S::kGpw + grp;
@@ -341,7 +517,8 @@ __device__ __forceinline__ void attn_tile(const unsigned char *Ks, const unsigne
         for (int c = 0; c < S::kCpl; ++c) Ty::widen2(raw[u][c], vf + c * P2);
         if constexpr (kMasked) {
             // Rows past the end of the chunk were not loaded: stale shared memory.
-            if (tile_k0 + warp * S::kKpw + u * S::kGpw + grp >= k_end) {
+            const int key = tile_k0 + warp * S::kKpw + u * S::kGpw + grp;
+            if (kMod ? key_unseen(mod, key, k_end) : key >= k_end) {
 #pragma unroll
                 for (int e = 0; e < E2; ++e) vf[e] = 0ull;
             }
@@ -420,7 +597,9 @@ __device__ __forceinline__ int owner_cta(long long t, long long n, long long G)
 // CTAs whose range crosses more head starts receive fewer tiles.  Per-head
 // values are computed once when the walk enters a head; a tile only costs a
 // few stores and the bulk copies.
-template <typename S, bool kWriteSeg, bool kPaged> struct RangeWalk {
+// kMod: only the tiles of the sequence's regions are walked (TileRegions).
+template <typename S, bool kWriteSeg, bool kPaged, bool kMod = false> struct RangeWalk {
+    TileRegions reg;        // kMod: of the current sequence
     long long t, hi, n, G;  // unit of the next tile, end of range, units in total, working CTAs
     int b, hr, tin, tb;     // sequence, head x row block, tile within the head, its tiles
     int HR;                 // H_kv * n_rowblocks
@@ -446,6 +625,7 @@ template <typename S, bool kWriteSeg, bool kPaged> struct RangeWalk {
 #endif
     const int32_t *bt_row;  // paged: block-table row of the current sequence
     const void *tm_k, *tm_v;  // tensor-map tiles (S::kTma): the K and V tensor maps
+    int window;               // kMod
 
     // Paged: start the load of the next tile's page-table entry; it is used
     // one fill later, so its latency hides behind the current tile.
@@ -453,8 +633,15 @@ template <typename S, bool kWriteSeg, bool kPaged> struct RangeWalk {
     {
         if constexpr (kPaged) {
             if (t < hi)
-                page_next = __ldg(bt_row + ((tin * S::kTK) >> a.page_shift));
+                page_next = __ldg(bt_row + ((tile_index() * S::kTK) >> a.page_shift));
         }
+    }
+
+    // The tile's place among all tiles of the sequence's keys.
+    __device__ __forceinline__ int tile_index() const
+    {
+        if constexpr (kMod) return reg.tile(tin);
+        else return tin;
     }
 
     __device__ __forceinline__ void enter_head(const AttnArgs &a, const int *pl)
@@ -465,6 +652,8 @@ template <typename S, bool kWriteSeg, bool kPaged> struct RangeWalk {
         if constexpr (kWriteSeg) {  // the split's shape, for the merge pass
             if (tin == 0) static_cast<int2 *>(a.merge_state)[(size_t)b * HR + hr] = make_int2(c_first, n_chunks);
         }
+        if constexpr (kMod)  // (the sequences' bounds follow the history lengths)
+            reg = tile_regions<S::kTK>(pl[b], a.N, window, pl[a.B + b], pl[2 * a.B + b]);
         set_head(a, pl[b]);
     }
 
@@ -572,7 +761,7 @@ template <typename S, bool kWriteSeg, bool kPaged> struct RangeWalk {
         TileMeta mt;
         mt.bh = bh;
         mt.rb = rb;
-        mt.tile_k0 = tin * S::kTK;
+        mt.tile_k0 = tile_index() * S::kTK;
         mt.nk = min(S::kTK, T_b - mt.tile_k0);
         mt.P = P;
         mt.flags = (piece_start ? kMetaFirst : 0) | ((tin == tb - 1 || t == hi - 1) ? kMetaLast : 0);
@@ -700,7 +889,7 @@ struct MergeJob {
 // are split over kNG thread groups when the head has fewer output elements
 // than the CTA has threads; the groups then combine through scr (shared
 // memory, free on entry and again on return).
-template <typename T, int D, int RB, int kThreads, bool kScaleV = false>
+template <typename T, int D, int RB, int kThreads, bool kScaleV = false, bool kMod = false>
 __device__ __forceinline__ void merge_pieces(const AttnArgs &a, const MergeJob &job, float *scr, int tid)
 {
     using Ty = Elem<T>;
@@ -771,7 +960,8 @@ __device__ __forceinline__ void merge_pieces(const AttnArgs &a, const MergeJob &
                     Ty::store(static_cast<T *>(a.out) + ((size_t)job.bh * a.rows + rg) * D + d,
                               num[i] / den[i] * a.kv_scale.y);
                 else
-                    Ty::store(static_cast<T *>(a.out) + ((size_t)job.bh * a.rows + rg) * D + d, num[i] / den[i]);
+                    Ty::store(static_cast<T *>(a.out) + ((size_t)job.bh * a.rows + rg) * D + d,
+                              quotient<kMod>(num[i], den[i]));
             }
         }
     }
@@ -781,8 +971,11 @@ __device__ __forceinline__ void merge_pieces(const AttnArgs &a, const MergeJob &
 // pre[b] = units of sequences 0..b-1 per head, pl[b] = P_b.  A sequence with
 // an invalid P_b gets no units; CTA 0 reports it, or (defer_error) returns
 // true for the caller to report later.
-template <typename S>
-__device__ __forceinline__ bool unit_prefix(const AttnArgs &a, int *pre, int *pl, int lane, bool defer_error = false)
+// kMod: the tiles of the sequence's regions count, and its bounds (seq_bounds)
+// are kept after pl.
+template <typename S, bool kMod = false>
+__device__ __forceinline__ bool unit_prefix(const AttnArgsOf<kMod> &a, int *pre, int *pl, int lane,
+                                            bool defer_error = false)
 {
     bool bad = false;
     int carry = 0;
@@ -797,7 +990,16 @@ __device__ __forceinline__ bool unit_prefix(const AttnArgs &a, int *pre, int *pl
                 if (defer_error) bad = true;
                 else raise_error(a.err_word, KVD_DEVERR_PAST_LEN);
             }
-            units = ok ? (P + a.N + S::kTK - 1) / S::kTK + S::kPieceUnits : 0;
+            if constexpr (kMod) {
+                if (ok) {
+                    const int2 db = seq_bounds(a, b, P);
+                    units = tile_regions<S::kTK>(P, a.N, a.window, db.x, db.y).n_tiles + S::kPieceUnits;
+                    pl[a.B + b] = db.x;
+                    pl[2 * a.B + b] = db.y;
+                }
+            } else {
+                units = ok ? (P + a.N + S::kTK - 1) / S::kTK + S::kPieceUnits : 0;
+            }
             pl[b] = P;
         }
         int v = units;  // inclusive scan over the warp
@@ -832,8 +1034,8 @@ __device__ __forceinline__ void cta_range(const AttnArgs &a, const int *pre, lon
 // marked to be skipped and the walk starts again.  Returns whether past_len
 // of the head's sequence is valid (else the range is empty and the sequence
 // is skipped).
-template <typename S, bool kPaged, typename Walk>
-__device__ __forceinline__ bool cluster_start(const AttnArgs &a, Walk &walk, unsigned char *smem, TileMeta *meta,
+template <typename S, bool kPaged, bool kMod, typename Walk>
+__device__ __forceinline__ bool cluster_start(const AttnArgsOf<kMod> &a, Walk &walk, unsigned char *smem, TileMeta *meta,
                                               uint64_t *full, int &issued, FillMode mode)
 {
     const int csize = (int)cluster_nctarank(), crank = (int)cluster_ctarank();
@@ -841,6 +1043,19 @@ __device__ __forceinline__ bool cluster_start(const AttnArgs &a, Walk &walk, uns
     const int u = (int)blockIdx.x / csize;  // the cluster's sequence-head (b, hr)
     const int b = u / HR, hr = u % HR;
     const int P = __ldg(a.past_len + b);  // (in flight during the fills below)
+    if constexpr (kMod) {  // (no speculation: the tiles depend on the sequence's bounds)
+        const bool ok = past_len_ok(P, a.N, a.T_max, a.max_past_len);
+        int tb = 0;
+        if (ok) {
+            const int2 db = seq_bounds(a, b, P);
+            walk.reg = tile_regions<S::kTK>(P, a.N, a.window, db.x, db.y);
+            tb = walk.reg.n_tiles;
+        }
+        walk.start_piece(a, b, hr, P, tb, tb * crank / csize, tb * (crank + 1) / csize, csize);
+        for (; issued < S::kStages && !walk.ended; ++issued)
+            walk.fill(a, nullptr, nullptr, smem, meta, full, issued, mode);
+        return ok;
+    }
     if constexpr (kPaged) {
         // (no speculation: block-table entries past a sequence's end need not
         // name valid pages)
@@ -880,11 +1095,13 @@ __device__ __forceinline__ bool cluster_start(const AttnArgs &a, Walk &walk, uns
 // piece into rank 0's shared memory, and rank 0 merges them (no workspace, no
 // atomics, one cluster barrier).  The pieces live after the fixed layout, in
 // place of the per-sequence tables: cluster size x RB rows of (o[D], m, l).
+// kMod: modified scores and per-row bounds (AttnScoredArgs), attention only.
 template <typename T, int D, int RB, bool kFused, bool kTicketMerge, bool kPaged, typename C = T,
-          bool kCluster = false>
+          bool kCluster = false, bool kMod = false>
 __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
-    attn_balanced_kernel(const AttnArgs a)
+    attn_balanced_kernel(const AttnArgsOf<kMod> a)
 {
+    static_assert(!kMod || (!kFused && std::is_same<T, C>::value), "modified scores: attention over T caches");
     using S = AttnShape<T, D, RB, C>;
     using Ty = Elem<C>;                                // cache rows
     using Tq = Elem<T>;                                // q / out rows
@@ -920,20 +1137,21 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
     // (slot s of ring position p is free again once every warp has released
     // position p - STAGES on empty[s]); the other warps go straight to
     // waiting for the first tile.
-    RangeWalk<S, !kTicketMerge, kPaged> walk;  // used by thread 0 only
+    RangeWalk<S, !kTicketMerge, kPaged, kMod> walk;  // used by thread 0 only
+    if constexpr (kMod) walk.window = a.window;
     int issued = 0;     // ring positions filled so far (thread 0)
     bool bad_past = false;
     int *cl_ok = reinterpret_cast<int *>(jobs);  // cluster mode: the head's sequence is valid
     if constexpr (kCluster) {
         // (planned for small layers only: the next kernel may launch now)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (stable && tid == 0) bad_past = !cluster_start<S, kPaged>(a, walk, smem, meta, full, issued, kFillKvOnly);
+        if (stable && tid == 0) bad_past = !cluster_start<S, kPaged, kMod>(a, walk, smem, meta, full, issued, kFillKvOnly);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (tid == 0) {
             if (stable) {
                 for (int p = 0; p < issued; ++p) walk.issue_pending(smem, full, p);  // the q rows
             } else {
-                bad_past = !cluster_start<S, kPaged>(a, walk, smem, meta, full, issued, kFillOne);
+                bad_past = !cluster_start<S, kPaged, kMod>(a, walk, smem, meta, full, issued, kFillOne);
             }
             *cl_ok = bad_past ? 0 : 1;
             ctl.described(issued);
@@ -950,7 +1168,7 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
         // previous kernel: start them before waiting.
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (stable && warp == 0) {
-            bad_past = unit_prefix<S>(a, pre, pl, lane, true);
+            bad_past = unit_prefix<S, kMod>(a, pre, pl, lane, true);
             if (lane == 0) {
                 long long n_total, G, lo, hi;
                 cta_range(a, pre, &n_total, &G, &lo, &hi);
@@ -974,7 +1192,7 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
     __syncthreads();  // barrier initialisation visible to every thread
 
     if (warp == 0 && !stable) {
-        unit_prefix<S>(a, pre, pl, lane);
+        unit_prefix<S, kMod>(a, pre, pl, lane);
         if (lane == 0) {
             long long n_total, G, lo, hi;
             cta_range(a, pre, &n_total, &G, &lo, &hi);
@@ -989,6 +1207,8 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
     f32x2 o[RB][S::kE / 2];
     float m_run[RB], l_run[RB];
     int lim[RB];
+    RowScore rs[kMod ? RB : 1];  // kMod: the rows' bounds and penalties ...
+    ModTile mod{};               // ... and the sequence's
     bool gave_up = false;     // this warp no longer waits for data (see AbortCtl)
     int first_unwaited = -1;  // thread 0: first ring position whose copies it did not see land
     int n_pieces = 0;         // split pieces computed so far (two at most)
@@ -1038,12 +1258,14 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
         const unsigned char *Vs = Ks + S::kTileBytes;
 
         if (mt.flags & kMetaFirst) {
+            if constexpr (kMod) mod = mod_tile(a, rs, mt.bh / a.H_kv, mt.P);
             const unsigned char *qs = smem + S::kQOff + s * S::kQSlotBytes;
             const int q_rows = min(RB, a.rows - mt.rb * RB);
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
                 const int rg = mt.rb * RB + r;
                 lim[r] = mt.P + 1 + (rg % a.N);
+                if constexpr (kMod) rs[r] = row_score(a, mt.bh / a.H_kv, mt.bh % a.H_kv, rg, mt.P);
                 m_run[r] = kNegInf;
                 l_run[r] = 0.f;
 #pragma unroll
@@ -1070,6 +1292,16 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
         // keys) take the unmasked path; the rest the masked one.  (A warp that
         // gave up computes nothing and writes nothing.)
         if (gave_up) {
+        } else if constexpr (kMod) {
+            bool all = true;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) all = all && row_sees_all<S::kTK>(rs[r], mod.pre, mt.tile_k0);
+            if (all && mt.nk == S::kTK)
+                attn_tile<T, D, RB, false, false, false, C, true>(Ks, Vs, qv, o, m_run, l_run, warp, grp, j, mt.tile_k0, lim, k_end,
+                                                                  mt.P, nullptr, nullptr, nullptr, nullptr, float2{}, mod);
+            else
+                attn_tile<T, D, RB, true, false, false, C, true>(Ks, Vs, qv, o, m_run, l_run, warp, grp, j, mt.tile_k0, lim, k_end,
+                                                                 mt.P, nullptr, nullptr, nullptr, nullptr, float2{}, mod);
         } else if (mt.tile_k0 + S::kTK <= mt.P + (kFused ? 0 : 1)) {
             attn_tile<T, D, RB, false, kFused, false, C>(Ks, Vs, qv, o, m_run, l_run, warp, grp, j, mt.tile_k0,
                                                          lim, k_end, mt.P, nullptr, nullptr, nullptr, nullptr);
@@ -1193,7 +1425,7 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
                     Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d,
                               num / den * a.kv_scale.y);
                 else
-                    Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d, num / den);
+                    Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d, quotient<kMod>(num, den));
             } else if constexpr (kCluster) {
                 float *pr = cl_part + r * (D + 2);
                 st_cluster_f32(pr + d, 0u, num);
@@ -1257,7 +1489,7 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
                         Tq::store(static_cast<T *>(a.out) + ((size_t)bh * a.rows + rg) * D + d,
                                   num / den * a.kv_scale.y);
                     else
-                        Tq::store(static_cast<T *>(a.out) + ((size_t)bh * a.rows + rg) * D + d, num / den);
+                        Tq::store(static_cast<T *>(a.out) + ((size_t)bh * a.rows + rg) * D + d, quotient<kMod>(num, den));
                 }
             }
         }
@@ -1287,8 +1519,8 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
         for (int i = 0; i < 2; ++i) {
             const MergeJob job = jobs[i];
             if (i < n_pieces && job.n_chunks)
-                merge_pieces<T, D, RB, S::kThreads, kQuant>(a, job, reinterpret_cast<float *>(smem + S::kEpiOff),
-                                                            tid);
+                merge_pieces<T, D, RB, S::kThreads, kQuant, kMod>(a, job, reinterpret_cast<float *>(smem + S::kEpiOff),
+                                                                  tid);
         }
     }
 
@@ -1315,7 +1547,7 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
 // one row per warp is best at 1024 rows, two at 8192 and 32768 rows.
 constexpr int kMergeRows = 2;
 
-template <typename T, int D, int RB, bool kScaleV = false>
+template <typename T, int D, int RB, bool kScaleV = false, bool kMod = false>
 __global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a)
 {
     using Ty = Elem<T>;
@@ -1416,7 +1648,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a)
                 if constexpr (kScaleV)
                     Ty::store(out + k, acc[i][k] / den[i] * a.kv_scale.y);
                 else
-                    Ty::store(out + k, acc[i][k] / den[i]);
+                    Ty::store(out + k, quotient<kMod>(acc[i][k], den[i]));
             }
         }
     }
@@ -1459,6 +1691,55 @@ template <typename T, int D, int RB, bool kTicketMerge, bool kPaged, typename C 
     v.piece_units = S::kPieceUnits;
     v.stages = S::kStages;
     return v;
+}
+
+// The same kernels with modified scores (kMod), attention only.
+template <typename T, int D, int RB, bool kTicketMerge, bool kPaged> AttnVariant make_scored_variant()
+{
+    using S = AttnShape<T, D, RB>;
+    AttnVariant v;
+    v.fn = reinterpret_cast<const void *>(&attn_balanced_kernel<T, D, RB, false, kTicketMerge, kPaged, T, false, true>);
+    v.fused_fn = nullptr;
+    if constexpr (kTicketMerge) {
+        v.merge_fn = nullptr;
+        v.cluster_fn = reinterpret_cast<const void *>(&attn_balanced_kernel<T, D, RB, false, true, kPaged, T, true, true>);
+    } else {
+        v.merge_fn = reinterpret_cast<const void *>(&attn_merge_kernel<T, D, RB, false, true>);
+    }
+    v.threads = S::kThreads;
+    v.fixed_smem_bytes = S::kFixedBytes;
+    v.tile_keys = S::kTK;
+    v.rows_per_block = RB;
+    v.piece_units = S::kPieceUnits;
+    v.stages = S::kStages;
+    return v;
+}
+
+template <typename T, int D, bool kTicketMerge, bool kPaged> bool pick_scored_rb(int RB, AttnVariant *v)
+{
+    switch (RB) {
+    case 1: *v = make_scored_variant<T, D, 1, kTicketMerge, kPaged>(); return true;
+    case 2: *v = make_scored_variant<T, D, 2, kTicketMerge, kPaged>(); return true;
+    case 4: *v = make_scored_variant<T, D, 4, kTicketMerge, kPaged>(); return true;
+    case 8:  // (16-bit rows of D = 128 take the tensor cores from 4 rows on)
+        if constexpr (sizeof(T) == 4 || D == 64) {
+            *v = make_scored_variant<T, D, 8, kTicketMerge, kPaged>();
+            return true;
+        } else {
+            return false;
+        }
+    default: return false;
+    }
+}
+
+template <typename T, bool kTicketMerge> bool pick_scored_variant(int D, int RB, bool paged, AttnVariant *v)
+{
+    switch (D) {
+    case 64: return paged ? pick_scored_rb<T, 64, kTicketMerge, true>(RB, v) : pick_scored_rb<T, 64, kTicketMerge, false>(RB, v);
+    case 128:
+        return paged ? pick_scored_rb<T, 128, kTicketMerge, true>(RB, v) : pick_scored_rb<T, 128, kTicketMerge, false>(RB, v);
+    default: return false;
+    }
 }
 
 template <typename T, int D, bool kTicketMerge, bool kPaged, typename C = T> bool pick_rb(int RB, AttnVariant *v)
@@ -1515,5 +1796,13 @@ bool attn_variant_tc5_bf16(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_bf16_tk(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_f16(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_f16_tk(int D, bool paged, AttnVariant *v);
+// modified scores: kvd_scored_{f32,bf16,f16}[_tk].cu (RB 1 .. 8: CUDA cores,
+// 16: mma.sync, 128: tcgen05)
+bool attn_variant_scored_f32(int D, int RB, bool paged, AttnVariant *v);
+bool attn_variant_scored_f32_tk(int D, int RB, bool paged, AttnVariant *v);
+bool attn_variant_scored_bf16(int D, int RB, bool paged, AttnVariant *v);
+bool attn_variant_scored_bf16_tk(int D, int RB, bool paged, AttnVariant *v);
+bool attn_variant_scored_f16(int D, int RB, bool paged, AttnVariant *v);
+bool attn_variant_scored_f16_tk(int D, int RB, bool paged, AttnVariant *v);
 
 }  // namespace kvd

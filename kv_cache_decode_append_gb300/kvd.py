@@ -60,6 +60,12 @@ class PlanInfo(ctypes.Structure):
                 ("cluster", ctypes.c_int)]
 
 
+class Score(ctypes.Structure):
+    """The C struct of the modified scores (kvd_decode_attention_scored)."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int),
+                ("doc_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
 class _Lib:
     """The loaded ``libkvd.so`` with typed C signatures."""
 
@@ -109,6 +115,13 @@ class _Lib:
         lib.kvd_rope_append.argtypes = [vp] * 9 + [ci, vp] + [ci] * 9 + [ci, u32p, vp]
         lib.kvd_paged_rope_append.restype = ci
         lib.kvd_paged_rope_append.argtypes = [vp] * 10 + [ci, vp] + [ci] * 11 + [ci, u32p, vp]
+        lib.kvd_decode_scored_workspace_bytes.restype = sz
+        lib.kvd_decode_scored_workspace_bytes.argtypes = [ci] * 7
+        lib.kvd_decode_attention_scored.restype = ci
+        lib.kvd_decode_attention_scored.argtypes = [vp] * 5 + [ctypes.POINTER(Score)] + [ci] * 7 + [cf, ci, vp, sz, u32p, vp]
+        lib.kvd_paged_decode_attention_scored.restype = ci
+        lib.kvd_paged_decode_attention_scored.argtypes = [vp] * 6 + [ctypes.POINTER(Score)] + [ci] * 9 + [cf, ci, vp, sz,
+                                                                                                        u32p, vp]
         lib.kvd_decode_attention_noalloc.restype = ci
         lib.kvd_decode_attention_noalloc.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, cf,
                                                      ci, u32p, vp]
@@ -663,6 +676,88 @@ def kvd_paged_rope_append(q, q_out, k_pages, v_pages, k_new, v_new, block_table,
                                    num_pages, int(max_past_len), _dtype_code(k_pages), _ptr(err_word),
                                    _stream_handle(stream))
     _check("kvd_paged_rope_append", st)
+
+
+# ---------------------------------------------------------------------------------
+# attention with modified scores
+def alloc_scored_workspace(B, H_q, H_kv, D, N, max_past_len, dtype, device=None) -> Optional[torch.Tensor]:
+    """A zero-filled device workspace for the scored attention calls with these shapes."""
+    code = _NAME_DTYPE[dtype] if isinstance(dtype, str) else _TORCH_DTYPE[dtype]
+    n = int(raw.kvd_decode_scored_workspace_bytes(B, H_q, H_kv, D, N, int(max_past_len), code))
+    if n == 0:
+        return None
+    return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def _score(q, softcap, slopes, window, doc_start, prefix_len) -> Score:
+    B, H_q, N, _ = q.shape
+    for n, t, dt, shape in (("slopes", slopes, torch.float32, (H_q,)), ("doc_start", doc_start, torch.int32, (B, N)),
+                            ("prefix_len", prefix_len, torch.int32, (B,))):
+        if t is not None:
+            _need_cuda(n, t, dt)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{n} must be {list(shape)}")
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be at least 0 and fit in 32 bits")
+    return Score(float(softcap), _ptr(slopes), int(window), _ptr(doc_start), _ptr(prefix_len))
+
+
+def kvd_decode_attention_scored(q, k_cache, v_cache, out, past_len, max_past_len: int, softcap: float = 0.0,
+                                slopes=None, window: int = 0, doc_start=None, prefix_len=None, scale: float = 0.0,
+                                workspace: Optional[torch.Tensor] = None, err_word=None, stream=None) -> None:
+    """kvd_decode_attention with modified scores, in any combination:
+
+    ``softcap`` > 0: scores capped to ``softcap * tanh(s / softcap)``; ``slopes`` fp32 [H_q]: a penalty
+    ``slopes[h] * |p - j|`` on the distance from a row's position p to key j; ``window`` > 0: a row sees
+    the last ``window`` keys up to its own; ``prefix_len`` int32 [B]: the first keys, seen by every row;
+    ``doc_start`` int32 [B, N]: a row sees no key before its document's first.  A row that sees no key
+    gets zeros.  Workspace: ``alloc_scored_workspace``."""
+    for n, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
+        _need_cuda(n, t, q.dtype)
+    _need_cuda("past_len", past_len, torch.int32)
+    if err_word is not None:
+        _need_cuda("err_word", err_word, torch.int32)
+    B, H_q, N, D = q.shape
+    _, H_kv, T_max, _ = k_cache.shape
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if past_len.numel() != B:
+        raise ValueError("past_len must hold B entries")
+    score = _score(q, softcap, slopes, window, doc_start, prefix_len)
+    _same_device(q, k_cache, v_cache, out, past_len, slopes, doc_start, prefix_len, workspace, err_word)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = raw.kvd_decode_attention_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+                                         past_len.data_ptr(), ctypes.byref(score), B, H_q, H_kv, T_max, D, N,
+                                         int(max_past_len), float(scale), _dtype_code(q), ws_ptr, ws_bytes,
+                                         _ptr(err_word), _stream_handle(stream))
+    _check("kvd_decode_attention_scored", st)
+
+
+def kvd_paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, past_len, max_past_len: int,
+                                      softcap: float = 0.0, slopes=None, window: int = 0, doc_start=None,
+                                      prefix_len=None, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
+                                      err_word=None, stream=None) -> None:
+    """kvd_decode_attention_scored over a paged cache; pages that hold only keys no row sees are not read."""
+    for n, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("out", out)):
+        _need_cuda(n, t, q.dtype)
+    _need_cuda("past_len", past_len, torch.int32)
+    if err_word is not None:
+        _need_cuda("err_word", err_word, torch.int32)
+    B, H_q, N, D = q.shape
+    num_pages, H_kv, page_size, Dp, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
+    if out.shape != q.shape or Dp != D:
+        raise ValueError("shape mismatch between q, out and the pages")
+    if past_len.numel() != B:
+        raise ValueError("past_len must hold B entries")
+    score = _score(q, softcap, slopes, window, doc_start, prefix_len)
+    _same_device(q, k_pages, v_pages, out, block_table, past_len, slopes, doc_start, prefix_len, workspace, err_word)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = raw.kvd_paged_decode_attention_scored(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+                                               block_table.data_ptr(), past_len.data_ptr(), ctypes.byref(score), B,
+                                               H_q, H_kv, D, N, page_size, max_pages, num_pages, int(max_past_len),
+                                               float(scale), _dtype_code(q), ws_ptr, ws_bytes, _ptr(err_word),
+                                               _stream_handle(stream))
+    _check("kvd_paged_decode_attention_scored", st)
 
 
 def kvd_decode_attention_noalloc(q, k_cache, v_cache, out, past_len, max_past_len: int,

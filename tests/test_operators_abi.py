@@ -68,3 +68,55 @@ def test_paged_rope_append_geometry(lib):
     assert _paged_rope(lib, max_pages=0) == INVALID
     assert _paged_rope(lib, num_pages=0) == INVALID
     assert _paged_rope(lib, max_pages=1 << 26) == INVALID
+
+
+class _Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int),
+                ("doc_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
+def _scored(lib, score=(), q=A, k=A, v=A, out=A, past=A, B=1, H_q=4, H_kv=2, T_max=64, D=64, N=1, max_past=10,
+            dtype=BF16):
+    s = None if score is None else ctypes.byref(_Score(*score))
+    return lib.kvd_decode_attention_scored(q, k, v, out, past, _cast(s), B, H_q, H_kv, T_max, D, N, max_past, 0.0,
+                                           dtype, None, 0, None, None)
+
+
+def _paged_scored(lib, score=(), q=A, k=A, v=A, out=A, table=A, past=A, B=1, H_q=4, H_kv=2, D=64, N=1, page_size=64,
+                  max_pages=1, num_pages=8, max_past=10, dtype=BF16):
+    s = None if score is None else ctypes.byref(_Score(*score))
+    return lib.kvd_paged_decode_attention_scored(q, k, v, out, table, past, _cast(s), B, H_q, H_kv, D, N, page_size,
+                                                 max_pages, num_pages, max_past, 0.0, dtype, None, 0, None, None)
+
+
+def _cast(s):
+    from kv_cache_decode_append_gb300 import kvd
+    return None if s is None else ctypes.cast(s, ctypes.POINTER(kvd.Score))
+
+
+@pytest.mark.parametrize("call", [_scored, _paged_scored])
+def test_scored_attention_refusals(lib, call):
+    assert call(lib, score=None) == INVALID
+    for name in ("q", "k", "v", "out", "past"):
+        assert call(lib, **{name: None}) == INVALID, name
+    for name in ("q", "k", "v", "out"):
+        assert call(lib, **{name: A + 8}) == INVALID, name
+    for cap in (-1.0, float("inf"), float("nan")):
+        assert call(lib, score=(cap,)) == INVALID
+    assert call(lib, score=(0.0, None, -1)) == INVALID
+    assert call(lib, score=(0.0, A + 2)) == INVALID
+    assert call(lib, score=(0.0, None, 0, A + 1)) == INVALID
+    assert call(lib, score=(0.0, None, 0, None, A + 3)) == INVALID
+    assert call(lib, H_q=3) == INVALID
+    assert call(lib, N=0) == INVALID
+    assert call(lib, D=96) == UNSUPPORTED
+    assert call(lib, dtype=E4M3) == UNSUPPORTED
+    assert call(lib, H_q=16, H_kv=1, N=65, max_past=0) == UNSUPPORTED
+    assert call(lib, max_past=64) == CAPACITY
+    assert call(lib, score=(2.0, A, 5, A, A), B=0) == OK
+
+
+def test_scored_workspace_query_rejects_bad_shapes(lib):
+    assert lib.kvd_decode_scored_workspace_bytes(1, 3, 2, 64, 1, 10, BF16) == 0
+    assert lib.kvd_decode_scored_workspace_bytes(1, 4, 2, 80, 1, 10, BF16) == 0
+    assert lib.kvd_decode_scored_workspace_bytes(1, 4, 2, 128, 1, 10, E4M3) == 0

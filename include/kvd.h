@@ -539,6 +539,47 @@ kvd_status kvd_paged_decode_attention_scored(const void *q, const void *k_pages,
                                              float scale, kvd_dtype dtype, void *workspace, size_t workspace_bytes,
                                              uint32_t *err_word, void *stream);
 
+/*
+ * kvd_shared_prefix_attention / kvd_paged_shared_prefix_attention --
+ * kvd_decode_attention of a batch whose sequences all begin with the same
+ * prefix, kept once: its keys and values are read once for the whole batch, the
+ * query rows of all sequences (B * (H_q / H_kv) * N per KV head) against them on
+ * the tensor cores (fp32: CUDA cores).  No counterpart in the source pages.
+ *
+ * For sequence b, query head hq, new row i, h = hq / (H_q / H_kv),
+ * P = past_len[b] (tokens in the sequence's own cache, before the append):
+ *   keys k_prefix[h, 0 .. prefix_len - 1], then k_cache[b, h, 0 .. P + i],
+ *   out[b,hq,i,:] = softmax(scale * q . keys) . values, as if they were one cache.
+ *
+ *   k_prefix, v_prefix  device, [H_kv, S_max, D], prefix_len <= S_max
+ *   prefix_table        paged: device int32, the ceil(prefix_len / page_size)
+ *                       pages of the prefix, in the same pool as the caches
+ *   prefix_len          host, >= 0 (0: the sequences' own keys alone)
+ *   workspace           of at least kvd_shared_prefix_workspace_bytes(...)
+ *                       bytes, 256-byte aligned; it needs no initial contents.
+ *                       Calls that run concurrently need distinct workspaces.
+ * Rows past prefix_len may hold anything.  Other arguments, limits, errors and
+ * device-side checks as for kvd_decode_attention (kvd_paged_decode_attention):
+ * (H_q / H_kv) * N <= 1024 rows per sequence, any B.  prefix_len > S_max, or more
+ * prefix pages than the pool has: KVD_ERR_CAPACITY.  Positions for a model that
+ * rotates: kvd_rope_append with pos_base = prefix_len.
+ */
+size_t kvd_shared_prefix_workspace_bytes(int B, int H_q, int H_kv, int D, int N, int prefix_len, int max_past_len,
+                                         kvd_dtype dtype);
+
+kvd_status kvd_shared_prefix_attention(const void *q, const void *k_prefix, const void *v_prefix, const void *k_cache,
+                                       const void *v_cache, void *out, const int32_t *past_len, int B, int H_q,
+                                       int H_kv, int S_max, int T_max, int D, int N, int prefix_len, int max_past_len,
+                                       float scale, kvd_dtype dtype, void *workspace, size_t workspace_bytes,
+                                       uint32_t *err_word, void *stream);
+
+kvd_status kvd_paged_shared_prefix_attention(const void *q, const void *k_pages, const void *v_pages, void *out,
+                                             const int32_t *prefix_table, const int32_t *block_table,
+                                             const int32_t *past_len, int B, int H_q, int H_kv, int D, int N,
+                                             int page_size, int max_pages, int num_pages, int prefix_len,
+                                             int max_past_len, float scale, kvd_dtype dtype, void *workspace,
+                                             size_t workspace_bytes, uint32_t *err_word, void *stream);
+
 /* kvd_workspace_init -- zero-fill a workspace on `stream` (asynchronous), as
  * kvd_decode_attention and kvd_decode_step need before a workspace's first use. */
 kvd_status kvd_workspace_init(void *workspace, size_t workspace_bytes, void *stream);

@@ -15,5 +15,6 @@ from .kvd import (  # noqa: F401
     kvd_paged_decode_attention, kvd_paged_decode_step, KVD_E4M3, kvd_append_e4m3,
     kvd_decode_attention_e4m3, kvd_decode_step_e4m3, kvd_rope_append, kvd_paged_rope_append,
     alloc_scored_workspace, kvd_decode_attention_scored, kvd_paged_decode_attention_scored,
+    alloc_shared_prefix_workspace, kvd_shared_prefix_attention, kvd_paged_shared_prefix_attention,
     kvd_status_string, kvd_workspace_init, library_path, load, raw,
 )

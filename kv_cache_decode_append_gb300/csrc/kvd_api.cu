@@ -151,6 +151,10 @@ int elem_bytes(kvd_dtype dt)
     }
 }
 
+#ifdef KVD_TIMEOUT_TEST
+int g_test_stall = 0;  // test builds: plant kArgTestStall in the next launches
+#endif
+
 kvd_status check_paged(const PagedCache &pc, int *T_max, int *page_shift)
 {
     if (pc.block_table == nullptr || pc.max_pages < 1 || pc.num_pages < 1) return KVD_ERR_INVALID_ARG;
@@ -363,10 +367,6 @@ kvd_status cluster_fits(int dev, const void *fn, int threads, int smem, int c, b
     return KVD_OK;
 }
 
-#ifdef KVD_TIMEOUT_TEST
-int g_test_stall = 0;  // test builds: plant kArgTestStall in the next launches
-#endif
-
 // The split-T plan of one decode_attention call.
 struct Plan {
     AttnVariant v;
@@ -378,7 +378,7 @@ struct Plan {
     bool tc5;         // tcgen05 kernel (128-row blocks, tiles and q by tensor map)
     bool early;       // small layer: kArgEarly, fewer CTAs per SM
     int cluster;      // > 0: cluster mode with this many CTAs per sequence-head
-    size_t part_off, tickets_off, seg_off, ws_bytes;
+    size_t part_off, tickets_off, seg_off, state_off, ws_bytes;
 };
 
 kvd_status check_shapes(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype)
@@ -439,9 +439,11 @@ bool pick_scored_builds(kvd_dtype dtype, int D, int rb, bool paged, AttnVariant 
 }
 
 // scored: the kernels with modified scores.  keys: an upper bound on the keys
-// a sequence's rows see together (0: max_past_len + N).
+// a sequence's rows see together (0: max_past_len + N).  states: the kernels
+// with modified scores leaving row states (no merge pass of their own, every
+// split described in the workspace).
 kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype,
-                     Plan *pl, bool paged = false, bool scored = false, long long keys = 0)
+                     Plan *pl, bool paged = false, bool scored = false, long long keys = 0, bool states = false)
 {
     kvd_status st = check_shapes(B, H_q, H_kv, D, N, max_past_len, dtype);
     if (st != KVD_OK) return st;
@@ -511,7 +513,7 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     // Small layers leave room on every SM for the calls that follow.
     const long long t_hint = keys > 0 ? keys : (long long)max_past_len + N;
     const long long kv_bytes_hint = 2LL * B * H_kv * t_hint * D * elem_bytes(dtype);
-    pl->early = !pl->mma && !pl->tc5 && kv_bytes_hint <= kEarlyMaxBytes;
+    pl->early = !states && !pl->mma && !pl->tc5 && kv_bytes_hint <= kEarlyMaxBytes;
     pl->grid = sms * (pl->early && occ > kEarlyCtasPerSm ? kEarlyCtasPerSm : occ);
     pl->max_tiles = (int)((t_hint + pl->v.tile_keys - 1) / pl->v.tile_keys);
     // Heads split across CTAs: merged inside the kernel by the CTA that
@@ -521,7 +523,7 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     // tail of the last CTA.
     const long long units_hint =
         (long long)B * H_kv * pl->n_rowblocks * (pl->max_tiles + pl->v.piece_units);
-    pl->merge_pass = !pl->early && units_hint > (long long)kLongRangeUnits * pl->grid;
+    pl->merge_pass = states || (!pl->early && units_hint > (long long)kLongRangeUnits * pl->grid);
     pl->launches = pl->merge_pass ? 2 : 1;
     if (!pl->merge_pass) pl->v = vt;
     pl->cluster = 0;
@@ -561,11 +563,42 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     off += round_up((size_t)B * H_kv * pl->n_rowblocks * sizeof(int), 256);
     pl->seg_off = off;
     off += round_up((size_t)B * H_kv * pl->n_rowblocks * sizeof(int2), 256);
+    pl->state_off = off;  // per query row: o[D], m, l, 2 floats of padding
+    if (states) off += round_up((size_t)B * H_q * N * (D + 4) * sizeof(float), 256);
     pl->ws_bytes = off;
     return KVD_OK;
 }
 
 }  // namespace
+
+kvd_status encode_map_16bit(CUtensorMap *map, const void *base, kvd_dtype dtype, int rank, const uint64_t *dims,
+                            const uint64_t *strides, const uint32_t *box)
+{
+    EncodeTiledFn fn;
+    const kvd_status st = encode_fn(&fn);
+    if (st != KVD_OK) return st;
+    cuuint64_t d[5], t[5];
+    cuuint32_t b[5], e[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        e[i] = 1;
+        if (i + 1 < rank) t[i] = strides[i];
+    }
+    const CUtensorMapDataType ty = dtype == KVD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(map, ty, (cuuint32_t)rank, const_cast<void *>(base), d, t, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? KVD_OK
+               : KVD_ERR_CUDA;
+}
+
+kvd_status kernel_ready(const void *fn, int threads, int smem)
+{
+    int dev = 0, occ = 0;
+    const kvd_status st = current_device(&dev);
+    return st != KVD_OK ? st : occupancy(dev, fn, threads, smem, &occ);
+}
 
 kvd_status current_sm_count(int *sms)
 {
@@ -702,8 +735,9 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
                          int T_max, int D, int N, int max_past_len, float scale, kvd_dtype dtype,
                          void *workspace, size_t workspace_bytes, uint32_t *err_word, void *stream,
                          const PagedCache *paged = nullptr, const float *e4m3_scales = nullptr,
-                         uint32_t step_flags = 0u, const kvd_score *score = nullptr)
+                         uint32_t step_flags = 0u, const kvd_score *score = nullptr, bool states = false)
 {
+    if (states) out = workspace;  // (row states in the workspace; no output is written)
     if (!q || !k_cache || !v_cache || !out || !past_len) return KVD_ERR_INVALID_ARG;
     kvd_status st = check_shapes(B, H_q, H_kv, D, N, max_past_len, dtype);
     if (st != KVD_OK) return st;
@@ -728,7 +762,8 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
     if (B == 0) return KVD_OK;
 
     Plan pl;
-    if ((st = make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, paged != nullptr, score != nullptr, keys)) != KVD_OK)
+    if ((st = make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, paged != nullptr, score != nullptr, keys,
+                        states)) != KVD_OK)
         return st;
     if (workspace == nullptr || workspace_bytes < pl.ws_bytes ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -780,6 +815,7 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
         a.cap = score->softcap * kLog2e;
         a.cap_in = score->softcap > 0.f ? 2.f / score->softcap : 0.f;  // (2 log2(e) / C)
         a.window = score->window;
+        a.row_state = states ? reinterpret_cast<float *>(ws + pl.state_off) : nullptr;
     }
 
     // Both kernels are programmatic dependents of whatever precedes them on
@@ -832,7 +868,7 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
     } else if (cudaLaunchKernelExC(&cfg, k_new != nullptr ? pl.v.fused_fn : pl.v.fn, args) != cudaSuccess) {
         return KVD_ERR_CUDA;
     }
-    if (pl.merge_pass) {
+    if (pl.merge_pass && !states) {
         // four-warp CTAs striding over the real query rows, a warp per row
         // up to kMergeCtasPerSm CTAs per SM (then kMergeRows rows per warp at
         // a time), so that the whole grid is resident soon after the
@@ -849,6 +885,52 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
 }
 
 }  // namespace
+
+namespace kvd {
+
+kvd_status row_state_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype, bool paged,
+                          RowStatePlan *plan)
+{
+    if (dtype == KVD_E4M3) return KVD_ERR_UNSUPPORTED;
+    Plan pl;
+    const kvd_status st = make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, paged, true, 0, true);
+    if (st != KVD_OK) return st;
+    plan->rb = pl.rb;
+    plan->n_rowblocks = pl.n_rowblocks;
+    plan->prow = pl.rb >= 16 && pl.rows < pl.rb ? pl.rows : pl.rb;  // (the kernels' part_rows)
+    plan->part_off = pl.part_off;
+    plan->seg_off = pl.seg_off;
+    plan->state_off = pl.state_off;
+    plan->bytes = pl.ws_bytes;
+    return KVD_OK;
+}
+
+kvd_status row_state_check(const void *q, const void *k_cache, const void *v_cache, const int32_t *past_len, int B,
+                           int H_q, int H_kv, int T_max, int D, int N, int max_past_len, kvd_dtype dtype,
+                           const PagedCache *paged)
+{
+    if (!q || !k_cache || !v_cache || !past_len) return KVD_ERR_INVALID_ARG;
+    kvd_status st = check_shapes(B, H_q, H_kv, D, N, max_past_len, dtype);
+    if (st != KVD_OK) return st;
+    if (dtype == KVD_E4M3) return KVD_ERR_UNSUPPORTED;
+    int page_shift = 0;
+    if (paged != nullptr && (st = check_paged(*paged, &T_max, &page_shift)) != KVD_OK) return st;
+    if (T_max < 1 || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return KVD_ERR_INVALID_ARG;
+    return (long long)max_past_len + N > T_max ? KVD_ERR_CAPACITY : KVD_OK;
+}
+
+kvd_status row_state_launch(const void *q, const void *k_cache, const void *v_cache, const int32_t *past_len, int B,
+                            int H_q, int H_kv, int T_max, int D, int N, int max_past_len, float scale,
+                            kvd_dtype dtype, const PagedCache *paged, void *workspace, size_t workspace_bytes,
+                            uint32_t *err_word, void *stream)
+{
+    const kvd_score none = {};
+    return decode_launch(q, k_cache, v_cache, nullptr, nullptr, nullptr, past_len, B, H_q, H_kv, T_max, D, N,
+                         max_past_len, scale, dtype, workspace, workspace_bytes, err_word, stream, paged, nullptr, 0u,
+                         &none, true);
+}
+
+}  // namespace kvd
 
 extern "C" {
 

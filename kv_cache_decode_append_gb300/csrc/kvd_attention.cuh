@@ -135,6 +135,8 @@ struct AttnScoredArgs : AttnArgs {
     float cap;                  // C, or 0: no cap
     float cap_in;               // 2 log2(e) / C
     int window;                 // 0: none
+    float *row_state;           // [B * H_q * N][D + 4] or null: rows of heads that lie in one CTA
+                                // leave their state here (o, m, l; for a join) instead of an output
 };
 template <bool kMod> using AttnArgsOf = typename std::conditional<kMod, AttnScoredArgs, AttnArgs>::type;
 
@@ -1419,6 +1421,17 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
                 const float wt = safe_weight(ep_m[w * RB + r], M);
                 num = fmaf(wt, ep_o[(w * RB + r) * D + d], num);
                 den = fmaf(wt, ep_l[w * RB + r], den);
+            }
+            if constexpr (kMod) {
+                if (single && a.row_state != nullptr) {
+                    float *pr = a.row_state + ((size_t)mt.bh * a.rows + rg) * (D + 4);
+                    pr[d] = num;
+                    if (d == 0) {
+                        pr[D] = M;
+                        pr[D + 1] = den;
+                    }
+                    continue;
+                }
             }
             if (single) {
                 if constexpr (kQuant)  // values are stored / v_scale

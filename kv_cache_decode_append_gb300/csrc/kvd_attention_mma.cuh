@@ -1001,6 +1001,17 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
                 num = fmaf(wt, ep_o[(w * RB + r) * D + d], num);
                 den = fmaf(wt, ep_l[w * RB + r], den);
             }
+            if constexpr (kMod) {
+                if (single && a.row_state != nullptr) {
+                    float *pr = a.row_state + ((size_t)mt.bh * a.rows + rg) * (D + 4);
+                    pr[d] = num;
+                    if (d == 0) {
+                        pr[D] = M;
+                        pr[D + 1] = den;
+                    }
+                    continue;
+                }
+            }
             if (single) {
                 if constexpr (k8)  // values are stored / v_scale
                     Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d, num / den * a.kv_scale.y);

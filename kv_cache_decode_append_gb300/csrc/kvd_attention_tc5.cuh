@@ -796,12 +796,19 @@ __global__ void __launch_bounds__(224, 1)
                         ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == mt.c_first ? 1 : 0)) * part_rows<S::kRB>(a.rows);
                     pr = a.part + (pbase + r) * (D + 4);
                 }
+                bool to_out = single;
+                if constexpr (kMod) {
+                    if (single && a.row_state != nullptr) {
+                        pr = a.row_state + ((size_t)mt.bh * a.rows + rg) * (D + 4);
+                        to_out = false;
+                    }
+                }
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
                     tc5_ld32(lane_addr + S::kTmemO + c0, o);
                     if (!real) continue;
-                    if (single) {
+                    if (to_out) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             stg128(orow + c0 + i,
@@ -815,7 +822,7 @@ __global__ void __launch_bounds__(224, 1)
                             *reinterpret_cast<uint4 *>(pr + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
-                if (real && !single) *reinterpret_cast<float2 *>(pr + D) = make_float2(m_run, l_run);
+                if (real && !to_out) *reinterpret_cast<float2 *>(pr + D) = make_float2(m_run, l_run);
             }
             tc5_fence_before();  // (the next arrive on p_full orders these reads before O is overwritten)
             if constexpr (kTicketMerge) {

@@ -1,0 +1,189 @@
+// kvd_prefix.cuh -- attention of a batch over one shared prefix.
+//
+// Every sequence of the batch attends the same prefix keys 0 .. S-1 before its
+// own cache.  Softmax splits over any partition of the keys: with (o, m, l) of a
+// part (o = sum 2^(y_j - m) v_j, l = sum 2^(y_j - m), y in log2 units),
+//   out = sum_parts 2^(m - M) o / sum_parts 2^(m - M) l,   M = max m,
+// so the call is three launches on one stream:
+//   1. the attention kernels over the sequences' own caches, which leave each
+//      row's state instead of an output (AttnScoredArgs::row_state);
+//   2. a prefix kernel over the B g N rows that each KV head has in the whole
+//      batch: a GEMM-shaped product that reads the prefix once (this file and
+//      kvd_prefix_tc5.cuh);
+//   3. prefix_join_kernel: the join of a row's prefix pieces and own state.
+//
+// Rows of the prefix kernels.  A KV head's rows are those of its gN rows in
+// every sequence (contiguous in q per sequence).  A block is 128 of them: with
+// gN <= 128, seqs = 128 / gN whole sequences (seqs gN rows are used); else 128
+// rows of one sequence.  A unit is one KV head with `unit_blocks` (1 or 2)
+// blocks.
+//
+// Split.  The (unit, key tile) pairs form one list, unit by unit; CTA c of G
+// takes [n c / G, n (c + 1) / G).  A unit's part in one CTA is a piece.  Along
+// the list either the unit or the CTA steps from one piece to the next, so piece
+// (u, c) has slot u + c: no slot is shared and there are at most units + G - 1.
+#pragma once
+
+#include "kvd_attention.cuh"
+
+namespace kvd {
+
+constexpr int kPrefixBlock = 128;  // rows of a block
+
+struct PrefixArgs {
+    const void *q;                // [B, H_kv, gN, D]
+    const void *k, *v;            // [H_kv, S_max, D], or the page pool
+    const int32_t *table;         // paged: pages of the prefix, else null
+    float *part;                  // pieces: [slot][(D / 4)][slot_rows] float4 (o), then ...
+    float *part_ml;               // ... [slot][2][slot_rows] (m, l)
+    uint32_t *err_word;
+    int B, H_kv, gN, S, S_max;
+    int seqs;                     // sequences per block (gN <= 128), else 1
+    int row_blocks;               // blocks per sequence (gN > 128), else 1
+    int blocks;                   // blocks per KV head
+    int unit_blocks, units_per_head, n_units;
+    int n_tiles;                  // key tiles of the prefix
+    int slot_rows;                // unit_blocks * 128
+    int page_shift, num_pages;
+    float qscale;                 // softmax scale * log2(e)
+    int flags;
+};
+constexpr int kPrefixTestStall = 1;  // (test builds only: see kArgTestStall)
+
+// First sequence and first of its rows of block k of a KV head.
+__device__ __forceinline__ int2 prefix_block_origin(const PrefixArgs &a, int k)
+{
+    return a.row_blocks == 1 ? make_int2(k * a.seqs, 0)
+                             : make_int2(k / a.row_blocks, (k % a.row_blocks) * kPrefixBlock);
+}
+
+// Sequence and row within it of row r of a block from `origin` (x < 0: none).
+__device__ __forceinline__ int2 prefix_block_row(const PrefixArgs &a, int2 origin, int r)
+{
+    int2 p = origin;
+    if (a.row_blocks == 1) {
+        p.x += r / a.gN;
+        p.y = r % a.gN;
+        if (r >= a.seqs * a.gN || p.x >= a.B) p.x = -1;
+    } else {
+        p.y += r;
+        if (p.y >= a.gN) p.x = -1;
+    }
+    return p;
+}
+
+// This CTA's range of the (unit, tile) list.
+__device__ __forceinline__ void prefix_range(const PrefixArgs &a, int *lo, int *hi)
+{
+    const long long n = (long long)a.n_units * a.n_tiles;
+    *lo = (int)(n * blockIdx.x / gridDim.x);
+    *hi = (int)(n * (blockIdx.x + 1) / gridDim.x);
+}
+
+// What the join needs of the attention kernels' row states.
+struct RowStateArgs {
+    const float *state;   // [B * H_kv * gN][D + 4]: rows of heads that lay in one CTA
+    const float *part;    // pieces of the others, as attn_merge_kernel reads them
+    const int2 *seg;      // (first CTA, CTAs) per (b, h, row block)
+    const int32_t *past_len;
+    int rb, n_rowblocks, prow, T_max, max_past_len, N, grid;  // grid: the prefix kernel's CTAs
+};
+
+// Join: out[b, h, y, :] of 32 rows of a block per CTA and a share of D.  A warp
+// takes groups of four columns (the pieces' layout: consecutive lanes are
+// consecutive rows), a lane one row.  Bound by reading the pieces (L2).
+constexpr int kJoinCols = 4;  // column groups (of 4) per warp
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a, const RowStateArgs s, void *out)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float kNegInf = __int_as_float(0xff800000);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int chunk = blockIdx.x % (kPrefixBlock / 32);
+    const int gb = blockIdx.x / (kPrefixBlock / 32);  // block of all heads
+    const int h = gb / a.blocks, k = gb % a.blocks;
+    const int u = h * a.units_per_head + k / a.unit_blocks;
+    const int r = chunk * 32 + lane;                          // row within the block
+    const int sr = (k % a.unit_blocks) * kPrefixBlock + r;    // row within the slot
+    const int2 p = prefix_block_row(a, prefix_block_origin(a, k), r);
+    if (p.x < 0) return;
+    const int P = __ldg(s.past_len + p.x);
+    if (!past_len_ok(P, s.N, s.T_max, s.max_past_len)) return;  // reported by the first launch
+    const int c0 = (blockIdx.y * 4 + warp) * kJoinCols;         // first column group
+
+    const long long n = (long long)a.n_units * a.n_tiles;
+    int first = 0, last = -1;  // CTAs that hold the unit's pieces (an empty prefix: none)
+    if (n > 0) {
+        first = owner_cta((long long)u * a.n_tiles, n, s.grid);
+        last = owner_cta((long long)(u + 1) * a.n_tiles - 1, n, s.grid);
+    }
+
+    float M = kNegInf, den = 0.f, acc[kJoinCols][4];
+#pragma unroll
+    for (int c = 0; c < kJoinCols; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+    auto add = [&](float m, float l, const float4 (&o)[kJoinCols]) {
+        const float Mn = fmaxf(M, m);
+        const float wa = safe_weight(M, Mn), wb = safe_weight(m, Mn);
+        den = den * wa + l * wb;
+#pragma unroll
+        for (int c = 0; c < kJoinCols; ++c) {
+            acc[c][0] = acc[c][0] * wa + o[c].x * wb;
+            acc[c][1] = acc[c][1] * wa + o[c].y * wb;
+            acc[c][2] = acc[c][2] * wa + o[c].z * wb;
+            acc[c][3] = acc[c][3] * wa + o[c].w * wb;
+        }
+        M = Mn;
+    };
+    const float4 *part = reinterpret_cast<const float4 *>(a.part);
+#pragma unroll 2
+    for (int c = first; c <= last; ++c) {
+        const size_t slot = (size_t)(u + c);
+        const float m = __ldcg(a.part_ml + (slot * 2) * a.slot_rows + sr);
+        const float l = __ldcg(a.part_ml + (slot * 2 + 1) * a.slot_rows + sr);
+        float4 o[kJoinCols];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) o[i] = __ldcg(part + (slot * (D / 4) + c0 + i) * a.slot_rows + sr);
+        add(m, l, o);
+    }
+    // the row's own keys
+    const int bh = p.x * a.H_kv + h;
+    const int2 seg = __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
+    for (int j = 0; j < seg.y; ++j) {
+        const float *pr = seg.y == 1 ? s.state + ((size_t)bh * a.gN + p.y) * (D + 4)
+                                     : s.part + (((size_t)(seg.x + j) * 2 + (j == 0)) * s.prow + p.y % s.rb) * (D + 4);
+        float4 o[kJoinCols];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) o[i] = __ldcg(reinterpret_cast<const float4 *>(pr) + c0 + i);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pr + D));
+        add(ml.x, ml.y, o);
+    }
+    T *row = static_cast<T *>(out) + ((size_t)bh * a.gN + p.y) * D + c0 * 4;
+    const float inv = 1.f / den;
+#pragma unroll
+    for (int c = 0; c < kJoinCols; ++c) {
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4 *>(row + 4 * c) =
+                make_float4(acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv);
+        else
+            *reinterpret_cast<uint2 *>(row + 4 * c) =
+                make_uint2(pack_pair<T>(acc[c][0] * inv, acc[c][1] * inv), pack_pair<T>(acc[c][2] * inv, acc[c][3] * inv));
+    }
+}
+
+// Launch facts of a prefix kernel, for the host.
+struct PrefixVariant {
+    const void *fn;
+    const void *join_fn;
+    int threads, smem_bytes, tile_keys, join_grid_y;
+    bool tma;  // takes the K, V and q tensor maps
+};
+
+bool prefix_variant_f32(int D, bool paged, PrefixVariant *v);
+bool prefix_variant_bf16(int D, bool paged, PrefixVariant *v);
+bool prefix_variant_f16(int D, bool paged, PrefixVariant *v);
+
+}  // namespace kvd

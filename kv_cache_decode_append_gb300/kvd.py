@@ -122,6 +122,12 @@ class _Lib:
         lib.kvd_paged_decode_attention_scored.restype = ci
         lib.kvd_paged_decode_attention_scored.argtypes = [vp] * 6 + [ctypes.POINTER(Score)] + [ci] * 9 + [cf, ci, vp, sz,
                                                                                                         u32p, vp]
+        lib.kvd_shared_prefix_workspace_bytes.restype = sz
+        lib.kvd_shared_prefix_workspace_bytes.argtypes = [ci] * 8
+        lib.kvd_shared_prefix_attention.restype = ci
+        lib.kvd_shared_prefix_attention.argtypes = [vp] * 7 + [ci] * 9 + [cf, ci, vp, sz, u32p, vp]
+        lib.kvd_paged_shared_prefix_attention.restype = ci
+        lib.kvd_paged_shared_prefix_attention.argtypes = [vp] * 7 + [ci] * 10 + [cf, ci, vp, sz, u32p, vp]
         lib.kvd_decode_attention_noalloc.restype = ci
         lib.kvd_decode_attention_noalloc.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, cf,
                                                      ci, u32p, vp]
@@ -758,6 +764,76 @@ def kvd_paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, pas
                                                float(scale), _dtype_code(q), ws_ptr, ws_bytes, _ptr(err_word),
                                                _stream_handle(stream))
     _check("kvd_paged_decode_attention_scored", st)
+
+
+# ---------------------------------------------------------------------------------
+# attention of a batch over one shared prefix
+def alloc_shared_prefix_workspace(B, H_q, H_kv, D, N, prefix_len: int, max_past_len, dtype,
+                                  device=None) -> Optional[torch.Tensor]:
+    """A device workspace for the shared-prefix attention calls with these shapes."""
+    code = _NAME_DTYPE[dtype] if isinstance(dtype, str) else _TORCH_DTYPE[dtype]
+    n = int(raw.kvd_shared_prefix_workspace_bytes(B, H_q, H_kv, D, N, int(prefix_len), int(max_past_len), code))
+    if n == 0:
+        return None
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def kvd_shared_prefix_attention(q, k_prefix, v_prefix, prefix_len: int, k_cache, v_cache, out, past_len,
+                                max_past_len: int, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
+                                err_word=None, stream=None) -> None:
+    """kvd_decode_attention of sequences that share their first ``prefix_len`` tokens: ``k_prefix`` and
+    ``v_prefix`` [H_kv, S_max, D] hold them once, the caches [B, H_kv, T_max, D] and ``past_len`` only what
+    follows.  Workspace: ``alloc_shared_prefix_workspace``."""
+    for n, t in (("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k_cache", k_cache), ("v_cache", v_cache),
+                 ("out", out)):
+        _need_cuda(n, t, q.dtype)
+    _need_cuda("past_len", past_len, torch.int32)
+    if err_word is not None:
+        _need_cuda("err_word", err_word, torch.int32)
+    B, H_q, N, D = q.shape
+    _, H_kv, T_max, _ = k_cache.shape
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if k_prefix.dim() != 3 or v_prefix.shape != k_prefix.shape or k_prefix.shape[0] != H_kv or k_prefix.shape[2] != D:
+        raise ValueError("k_prefix and v_prefix must be the same [H_kv, S_max, D]")
+    if past_len.numel() != B:
+        raise ValueError("past_len must hold B entries")
+    _same_device(q, k_prefix, v_prefix, k_cache, v_cache, out, past_len, workspace, err_word)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = raw.kvd_shared_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
+                                         v_cache.data_ptr(), out.data_ptr(), past_len.data_ptr(), B, H_q, H_kv,
+                                         k_prefix.shape[1], T_max, D, N, int(prefix_len), int(max_past_len),
+                                         float(scale), _dtype_code(q), ws_ptr, ws_bytes, _ptr(err_word),
+                                         _stream_handle(stream))
+    _check("kvd_shared_prefix_attention", st)
+
+
+def kvd_paged_shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len: int, out, block_table, past_len,
+                                      max_past_len: int, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
+                                      err_word=None, stream=None) -> None:
+    """kvd_shared_prefix_attention over a page pool: ``prefix_table`` int32 names the prefix's pages."""
+    for n, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("out", out)):
+        _need_cuda(n, t, q.dtype)
+    _need_cuda("past_len", past_len, torch.int32)
+    _need_cuda("prefix_table", prefix_table, torch.int32)
+    if err_word is not None:
+        _need_cuda("err_word", err_word, torch.int32)
+    B, H_q, N, D = q.shape
+    num_pages, H_kv, page_size, Dp, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
+    if out.shape != q.shape or Dp != D:
+        raise ValueError("shape mismatch between q, out and the pages")
+    if past_len.numel() != B:
+        raise ValueError("past_len must hold B entries")
+    if prefix_table.numel() * page_size < prefix_len:
+        raise ValueError("prefix_table must name every page of the prefix")
+    _same_device(q, k_pages, v_pages, prefix_table, out, block_table, past_len, workspace, err_word)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = raw.kvd_paged_shared_prefix_attention(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+                                               prefix_table.data_ptr(), block_table.data_ptr(), past_len.data_ptr(), B,
+                                               H_q, H_kv, D, N, page_size, max_pages, num_pages, int(prefix_len),
+                                               int(max_past_len), float(scale), _dtype_code(q), ws_ptr, ws_bytes,
+                                               _ptr(err_word), _stream_handle(stream))
+    _check("kvd_paged_shared_prefix_attention", st)
 
 
 def kvd_decode_attention_noalloc(q, k_cache, v_cache, out, past_len, max_past_len: int,

@@ -120,3 +120,45 @@ def test_scored_workspace_query_rejects_bad_shapes(lib):
     assert lib.kvd_decode_scored_workspace_bytes(1, 3, 2, 64, 1, 10, BF16) == 0
     assert lib.kvd_decode_scored_workspace_bytes(1, 4, 2, 80, 1, 10, BF16) == 0
     assert lib.kvd_decode_scored_workspace_bytes(1, 4, 2, 128, 1, 10, E4M3) == 0
+
+
+def _prefix(lib, q=A, kp=A, vp=A, k=A, v=A, out=A, past=A, B=1, H_q=4, H_kv=2, S_max=64, T_max=64, D=64, N=1, S=10,
+            max_past=10, dtype=BF16):
+    return lib.kvd_shared_prefix_attention(q, kp, vp, k, v, out, past, B, H_q, H_kv, S_max, T_max, D, N, S, max_past,
+                                           0.0, dtype, None, 0, None, None)
+
+
+def _paged_prefix(lib, q=A, k=A, v=A, out=A, ptable=A, table=A, past=A, B=1, H_q=4, H_kv=2, D=64, N=1, page_size=64,
+                  max_pages=1, num_pages=8, S=10, max_past=10, dtype=BF16):
+    return lib.kvd_paged_shared_prefix_attention(q, k, v, out, ptable, table, past, B, H_q, H_kv, D, N, page_size,
+                                                 max_pages, num_pages, S, max_past, 0.0, dtype, None, 0, None, None)
+
+
+@pytest.mark.parametrize("call", [_prefix, _paged_prefix])
+def test_shared_prefix_refusals(lib, call):
+    for name in ("q", "k", "v", "out", "past"):
+        assert call(lib, **{name: None}) == INVALID, name
+    for name in ("q", "k", "v", "out"):
+        assert call(lib, **{name: A + 8}) == INVALID, name
+    assert call(lib, S=-1) == INVALID
+    assert call(lib, H_q=3) == INVALID
+    assert call(lib, N=0) == INVALID
+    assert call(lib, B=-1) == INVALID
+    assert call(lib, D=96) == UNSUPPORTED
+    assert call(lib, dtype=E4M3) == UNSUPPORTED
+    assert call(lib, H_q=16, H_kv=1, N=65, max_past=0) == UNSUPPORTED
+    assert call(lib, max_past=64) == CAPACITY
+    assert call(lib, B=0) == OK
+
+
+def test_shared_prefix_refuses_its_own_arguments(lib):
+    assert _prefix(lib, kp=None) == INVALID
+    assert _prefix(lib, vp=A + 4) == INVALID
+    assert _prefix(lib, S=65) == CAPACITY
+    assert _prefix(lib, kp=None, vp=None, S=0, B=0) == OK
+    assert _paged_prefix(lib, ptable=None) == INVALID
+    assert _paged_prefix(lib, ptable=A + 2) == INVALID
+    assert _paged_prefix(lib, S=8 * 64 + 1) == CAPACITY
+    assert _paged_prefix(lib, page_size=32) == INVALID
+    assert lib.kvd_shared_prefix_workspace_bytes(1, 4, 2, 64, 1, -1, 10, BF16) == 0
+    assert lib.kvd_shared_prefix_workspace_bytes(1, 3, 2, 64, 1, 10, 10, BF16) == 0

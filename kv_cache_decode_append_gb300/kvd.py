@@ -170,7 +170,10 @@ def load() -> _Lib:
 
 class _Raw:
     def __getattr__(self, name):
-        return getattr(load(), name)
+        # (kept: the next look-up finds it without a call)
+        f = getattr(load(), name)
+        setattr(self, name, f)
+        return f
 
 
 raw = _Raw()
@@ -182,8 +185,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream_handle(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle (torch.cuda.current_stream() makes an object: 3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -591,54 +594,76 @@ def kvd_decode_step_e4m3(q, k_cache, v_cache, k_new, v_new, out, past_len, max_p
 
 # ---------------------------------------------------------------------------------
 # rotated append
-def _same_device(*tensors) -> None:
-    """The tensors (None skipped) lie on one device, the current one: the library launches there."""
+def _ready(t, dtype, dev: int) -> bool:
+    """A contiguous CUDA tensor of this dtype on this device."""
+    return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and t.get_device() == dev)
+
+
+def _refuse(dev: int, *named) -> None:
+    """Raise for the first of (name, tensor, dtype) that is not _ready on the current device."""
+    for n, t, dt in named:
+        if t is not None:
+            _need_cuda(n, t, dt)
+            if t.get_device() != dev:
+                raise ValueError(f"{n} must be on the current CUDA device (cuda:{dev}), got {t.device}")
+
+
+def _need_ready(*named) -> None:
+    """Every (name, tensor, dtype), None skipped, is a contiguous CUDA tensor of its dtype on the current
+    device, where the library launches."""
     dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{dev}), got {t.device}")
+    for n, t, dt in named:
+        if t is not None and not _ready(t, dt, dev):
+            _refuse(dev, (n, t, dt))
 
 
 def _need_rows(name: str, t: torch.Tensor, dtype) -> None:
-    """[B, H, N, D] rows: each row contiguous, the rows at any non-negative strides."""
+    """[B, H, N, D] rows on the current device: each row contiguous, the rows at any non-negative strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
         raise ValueError(f"{name} must be [B, H, N, D] with contiguous rows")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
 
 
 def _rope_rows(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, pos_base, positions, err_word):
     """Checks common to the rotated appends; returns (B, H_q, H_kv, N, D, strides or None)."""
     dt = k_cache.dtype
-    for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
-        _need_rows(n, t, dt)
-    for n, t in (("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache)):
-        _need_cuda(n, t, dt)
-    _need_cuda("past_len", past_len, torch.int32)
-    _need_cuda("inv_freq", inv_freq, torch.float64)
+    dev = torch.cuda.current_device()
+    dense = _ready(q, dt, dev) and _ready(k_new, dt, dev) and _ready(v_new, dt, dev)
+    if not dense or q.dim() != 4:
+        for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
+            _need_rows(n, t, dt)
+    if not (_ready(q_out, dt, dev) and _ready(k_cache, dt, dev) and _ready(v_cache, dt, dev)
+            and _ready(past_len, torch.int32, dev) and _ready(inv_freq, torch.float64, dev)):
+        _refuse(dev, ("q_out", q_out, dt), ("k_cache", k_cache, dt), ("v_cache", v_cache, dt),
+                ("past_len", past_len, torch.int32), ("inv_freq", inv_freq, torch.float64))
     B, H_q, N, D = q.shape
-    H_kv = k_new.shape[1]
+    new = k_new.shape
+    H_kv = new[1]
     if positions is not None:
-        _need_cuda("positions", positions, torch.int32)
+        _need_ready(("positions", positions, torch.int32))
         if tuple(positions.shape) != (B, N):
             raise ValueError("positions must be [B, N]")
     if err_word is not None:
-        _need_cuda("err_word", err_word, torch.int32)
-    if tuple(k_new.shape) != (B, H_kv, N, D) or v_new.shape != k_new.shape or q_out.shape != q.shape:
+        _need_ready(("err_word", err_word, torch.int32))
+    if new != (B, H_kv, N, D) or v_new.shape != new or q_out.shape != q.shape:
         raise ValueError("shape mismatch between q, q_out and the new K/V")
-    if v_cache.shape != k_cache.shape or k_cache.dim() != 4 or k_cache.shape[1] != H_kv or k_cache.shape[3] != D:
+    cache = k_cache.shape
+    if v_cache.shape != cache or len(cache) != 4 or cache[1] != H_kv or cache[3] != D:
         raise ValueError("shape mismatch between the caches and the new K/V")
     if past_len.numel() != B:
         raise ValueError("past_len must hold B entries")
-    _same_device(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, positions, err_word)
     if not -(1 << 31) <= pos_base < 1 << 31:
         raise ValueError("pos_base must fit in 32 bits")
+    if dense:
+        return B, H_q, H_kv, N, D, None
     if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
         raise ValueError("q_out may be q only when q is contiguous")
-    if q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous():
-        return B, H_q, H_kv, N, D, None
     # (a dimension of one row has no stride that matters; torch may report any)
     st = [s if n > 1 else 0 for t in (q, k_new, v_new) for s, n in zip(t.stride()[:3], t.shape[:3])]
     return B, H_q, H_kv, N, D, (ctypes.c_int64 * 9)(*st)
@@ -674,7 +699,7 @@ def kvd_paged_rope_append(q, q_out, k_pages, v_pages, k_new, v_new, block_table,
     B, H_q, H_kv, N, D, strides = _rope_rows(q, q_out, k_new, v_new, k_pages, v_pages, past_len, inv_freq, pos_base,
                                              positions, err_word)
     num_pages, _, page_size, _, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
-    _same_device(block_table)
+    _need_ready(("block_table", block_table, torch.int32))
     st = raw.kvd_paged_rope_append(q.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                    k_new.data_ptr(), v_new.data_ptr(), strides, block_table.data_ptr(),
                                    past_len.data_ptr(), _ptr(positions), int(pos_base), inv_freq.data_ptr(),
@@ -700,8 +725,8 @@ def _score(q, softcap, slopes, window, doc_start, prefix_len) -> Score:
     for n, t, dt, shape in (("slopes", slopes, torch.float32, (H_q,)), ("doc_start", doc_start, torch.int32, (B, N)),
                             ("prefix_len", prefix_len, torch.int32, (B,))):
         if t is not None:
-            _need_cuda(n, t, dt)
-            if tuple(t.shape) != shape:
+            _need_ready((n, t, dt))
+            if t.shape != shape:
                 raise ValueError(f"{n} must be {list(shape)}")
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be at least 0 and fit in 32 bits")
@@ -718,11 +743,9 @@ def kvd_decode_attention_scored(q, k_cache, v_cache, out, past_len, max_past_len
     the last ``window`` keys up to its own; ``prefix_len`` int32 [B]: the first keys, seen by every row;
     ``doc_start`` int32 [B, N]: a row sees no key before its document's first.  A row that sees no key
     gets zeros.  Workspace: ``alloc_scored_workspace``."""
-    for n, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
-        _need_cuda(n, t, q.dtype)
-    _need_cuda("past_len", past_len, torch.int32)
-    if err_word is not None:
-        _need_cuda("err_word", err_word, torch.int32)
+    dt = q.dtype
+    _need_ready(("q", q, dt), ("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("out", out, dt),
+                ("past_len", past_len, torch.int32), ("workspace", workspace, torch.uint8), ("err_word", err_word, torch.int32))
     B, H_q, N, D = q.shape
     _, H_kv, T_max, _ = k_cache.shape
     if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
@@ -730,7 +753,6 @@ def kvd_decode_attention_scored(q, k_cache, v_cache, out, past_len, max_past_len
     if past_len.numel() != B:
         raise ValueError("past_len must hold B entries")
     score = _score(q, softcap, slopes, window, doc_start, prefix_len)
-    _same_device(q, k_cache, v_cache, out, past_len, slopes, doc_start, prefix_len, workspace, err_word)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = raw.kvd_decode_attention_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                                          past_len.data_ptr(), ctypes.byref(score), B, H_q, H_kv, T_max, D, N,
@@ -744,11 +766,10 @@ def kvd_paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, pas
                                       prefix_len=None, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
                                       err_word=None, stream=None) -> None:
     """kvd_decode_attention_scored over a paged cache; pages that hold only keys no row sees are not read."""
-    for n, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("out", out)):
-        _need_cuda(n, t, q.dtype)
-    _need_cuda("past_len", past_len, torch.int32)
-    if err_word is not None:
-        _need_cuda("err_word", err_word, torch.int32)
+    dt = q.dtype
+    _need_ready(("q", q, dt), ("k_pages", k_pages, dt), ("v_pages", v_pages, dt), ("out", out, dt),
+                ("block_table", block_table, torch.int32), ("past_len", past_len, torch.int32),
+                ("workspace", workspace, torch.uint8), ("err_word", err_word, torch.int32))
     B, H_q, N, D = q.shape
     num_pages, H_kv, page_size, Dp, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
     if out.shape != q.shape or Dp != D:
@@ -756,7 +777,6 @@ def kvd_paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, pas
     if past_len.numel() != B:
         raise ValueError("past_len must hold B entries")
     score = _score(q, softcap, slopes, window, doc_start, prefix_len)
-    _same_device(q, k_pages, v_pages, out, block_table, past_len, slopes, doc_start, prefix_len, workspace, err_word)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = raw.kvd_paged_decode_attention_scored(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
                                                block_table.data_ptr(), past_len.data_ptr(), ctypes.byref(score), B,
@@ -784,12 +804,10 @@ def kvd_shared_prefix_attention(q, k_prefix, v_prefix, prefix_len: int, k_cache,
     """kvd_decode_attention of sequences that share their first ``prefix_len`` tokens: ``k_prefix`` and
     ``v_prefix`` [H_kv, S_max, D] hold them once, the caches [B, H_kv, T_max, D] and ``past_len`` only what
     follows.  Workspace: ``alloc_shared_prefix_workspace``."""
-    for n, t in (("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k_cache", k_cache), ("v_cache", v_cache),
-                 ("out", out)):
-        _need_cuda(n, t, q.dtype)
-    _need_cuda("past_len", past_len, torch.int32)
-    if err_word is not None:
-        _need_cuda("err_word", err_word, torch.int32)
+    dt = q.dtype
+    _need_ready(("q", q, dt), ("k_prefix", k_prefix, dt), ("v_prefix", v_prefix, dt), ("k_cache", k_cache, dt),
+                ("v_cache", v_cache, dt), ("out", out, dt), ("past_len", past_len, torch.int32),
+                ("workspace", workspace, torch.uint8), ("err_word", err_word, torch.int32))
     B, H_q, N, D = q.shape
     _, H_kv, T_max, _ = k_cache.shape
     if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
@@ -798,7 +816,6 @@ def kvd_shared_prefix_attention(q, k_prefix, v_prefix, prefix_len: int, k_cache,
         raise ValueError("k_prefix and v_prefix must be the same [H_kv, S_max, D]")
     if past_len.numel() != B:
         raise ValueError("past_len must hold B entries")
-    _same_device(q, k_prefix, v_prefix, k_cache, v_cache, out, past_len, workspace, err_word)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = raw.kvd_shared_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
                                          v_cache.data_ptr(), out.data_ptr(), past_len.data_ptr(), B, H_q, H_kv,
@@ -812,12 +829,11 @@ def kvd_paged_shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_
                                       max_past_len: int, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
                                       err_word=None, stream=None) -> None:
     """kvd_shared_prefix_attention over a page pool: ``prefix_table`` int32 names the prefix's pages."""
-    for n, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages), ("out", out)):
-        _need_cuda(n, t, q.dtype)
-    _need_cuda("past_len", past_len, torch.int32)
-    _need_cuda("prefix_table", prefix_table, torch.int32)
-    if err_word is not None:
-        _need_cuda("err_word", err_word, torch.int32)
+    dt = q.dtype
+    _need_ready(("q", q, dt), ("k_pages", k_pages, dt), ("v_pages", v_pages, dt), ("out", out, dt),
+                ("prefix_table", prefix_table, torch.int32), ("block_table", block_table, torch.int32),
+                ("past_len", past_len, torch.int32), ("workspace", workspace, torch.uint8),
+                ("err_word", err_word, torch.int32))
     B, H_q, N, D = q.shape
     num_pages, H_kv, page_size, Dp, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
     if out.shape != q.shape or Dp != D:
@@ -826,7 +842,6 @@ def kvd_paged_shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_
         raise ValueError("past_len must hold B entries")
     if prefix_table.numel() * page_size < prefix_len:
         raise ValueError("prefix_table must name every page of the prefix")
-    _same_device(q, k_pages, v_pages, prefix_table, out, block_table, past_len, workspace, err_word)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = raw.kvd_paged_shared_prefix_attention(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
                                                prefix_table.data_ptr(), block_table.data_ptr(), past_len.data_ptr(), B,

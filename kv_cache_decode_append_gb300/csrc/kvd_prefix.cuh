@@ -89,13 +89,15 @@ struct RowStateArgs {
     int rb, n_rowblocks, prow, T_max, max_past_len, N, grid;  // grid: the prefix kernel's CTAs
 };
 
-// Join: out[b, h, y, :] of 32 rows of a block per CTA and a share of D.  A warp
-// takes groups of four columns (the pieces' layout: consecutive lanes are
-// consecutive rows), a lane one row.  Bound by reading the pieces (L2).
-constexpr int kJoinCols = 4;  // column groups (of 4) per warp
+// Join: out[b, h, y, :] of 32 rows of a block and 32 columns per CTA: a warp
+// takes four columns (the pieces' layout: consecutive lanes are consecutive
+// rows), a lane one row.  Bound by the latency of reading the pieces (L2): the
+// loads of kJoinBatch pieces are in flight together.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a, const RowStateArgs s, void *out)
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixArgs a, const RowStateArgs s, void *out)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -109,9 +111,11 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a, co
     const int sr = (k % a.unit_blocks) * kPrefixBlock + r;    // row within the slot
     const int2 p = prefix_block_row(a, prefix_block_origin(a, k), r);
     if (p.x < 0) return;
+    const int c0 = blockIdx.y * (kJoinThreads / 32) + warp;   // column group
+    const int bh = p.x * a.H_kv + h;
     const int P = __ldg(s.past_len + p.x);
+    const int2 seg = __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
     if (!past_len_ok(P, s.N, s.T_max, s.max_past_len)) return;  // reported by the first launch
-    const int c0 = (blockIdx.y * 4 + warp) * kJoinCols;         // first column group
 
     const long long n = (long long)a.n_units * a.n_tiles;
     int first = 0, last = -1;  // CTAs that hold the unit's pieces (an empty prefix: none)
@@ -119,59 +123,47 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const PrefixArgs a, co
         first = owner_cta((long long)u * a.n_tiles, n, s.grid);
         last = owner_cta((long long)(u + 1) * a.n_tiles - 1, n, s.grid);
     }
-
-    float M = kNegInf, den = 0.f, acc[kJoinCols][4];
-#pragma unroll
-    for (int c = 0; c < kJoinCols; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-    auto add = [&](float m, float l, const float4 (&o)[kJoinCols]) {
+    float M = kNegInf, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float m, float l, const float4 &o) {
         const float Mn = fmaxf(M, m);
         const float wa = safe_weight(M, Mn), wb = safe_weight(m, Mn);
         den = den * wa + l * wb;
-#pragma unroll
-        for (int c = 0; c < kJoinCols; ++c) {
-            acc[c][0] = acc[c][0] * wa + o[c].x * wb;
-            acc[c][1] = acc[c][1] * wa + o[c].y * wb;
-            acc[c][2] = acc[c][2] * wa + o[c].z * wb;
-            acc[c][3] = acc[c][3] * wa + o[c].w * wb;
-        }
+        acc.x = acc.x * wa + o.x * wb;
+        acc.y = acc.y * wa + o.y * wb;
+        acc.z = acc.z * wa + o.z * wb;
+        acc.w = acc.w * wa + o.w * wb;
         M = Mn;
     };
-    const float4 *part = reinterpret_cast<const float4 *>(a.part);
-#pragma unroll 2
-    for (int c = first; c <= last; ++c) {
-        const size_t slot = (size_t)(u + c);
-        const float m = __ldcg(a.part_ml + (slot * 2) * a.slot_rows + sr);
-        const float l = __ldcg(a.part_ml + (slot * 2 + 1) * a.slot_rows + sr);
-        float4 o[kJoinCols];
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) o[i] = __ldcg(part + (slot * (D / 4) + c0 + i) * a.slot_rows + sr);
-        add(m, l, o);
-    }
     // the row's own keys
-    const int bh = p.x * a.H_kv + h;
-    const int2 seg = __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
     for (int j = 0; j < seg.y; ++j) {
         const float *pr = seg.y == 1 ? s.state + ((size_t)bh * a.gN + p.y) * (D + 4)
                                      : s.part + (((size_t)(seg.x + j) * 2 + (j == 0)) * s.prow + p.y % s.rb) * (D + 4);
-        float4 o[kJoinCols];
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) o[i] = __ldcg(reinterpret_cast<const float4 *>(pr) + c0 + i);
+        const float4 o = __ldcg(reinterpret_cast<const float4 *>(pr) + c0);
         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pr + D));
         add(ml.x, ml.y, o);
     }
+    const float4 *part = reinterpret_cast<const float4 *>(a.part);
+    for (int c = first; c <= last; c += kJoinBatch) {
+        float m[kJoinBatch], l[kJoinBatch];
+        float4 o[kJoinBatch];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const size_t slot = (size_t)(u + min(c + i, last));
+            m[i] = __ldcg(a.part_ml + (slot * 2) * a.slot_rows + sr);
+            l[i] = __ldcg(a.part_ml + (slot * 2 + 1) * a.slot_rows + sr);
+            o[i] = __ldcg(part + (slot * (D / 4) + c0) * a.slot_rows + sr);
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (c + i <= last) add(m[i], l[i], o[i]);
+    }
     T *row = static_cast<T *>(out) + ((size_t)bh * a.gN + p.y) * D + c0 * 4;
     const float inv = 1.f / den;
-#pragma unroll
-    for (int c = 0; c < kJoinCols; ++c) {
-        if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float4 *>(row + 4 * c) =
-                make_float4(acc[c][0] * inv, acc[c][1] * inv, acc[c][2] * inv, acc[c][3] * inv);
-        else
-            *reinterpret_cast<uint2 *>(row + 4 * c) =
-                make_uint2(pack_pair<T>(acc[c][0] * inv, acc[c][1] * inv), pack_pair<T>(acc[c][2] * inv, acc[c][3] * inv));
-    }
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(row) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else
+        *reinterpret_cast<uint2 *>(row) = make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv), pack_pair<T>(acc.z * inv, acc.w * inv));
 }
 
 // Launch facts of a prefix kernel, for the host.

@@ -85,8 +85,7 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     if (workspace == nullptr || workspace_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return KVD_ERR_WORKSPACE;
     const int gN = H_q / H_kv * N;
-    const long long rows = paged != nullptr ? (long long)paged->num_pages * H_kv * paged->page_size : (long long)H_kv * S_max;
-    if (pl.v.tma && S > 0 && rows + 64 > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;  // 32-bit box coordinates
+    if (pl.v.tma && (long long)S + 128 > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;  // 32-bit box coordinates
 
     char *ws = static_cast<char *>(workspace);
     PrefixArgs a = {};
@@ -117,14 +116,21 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     if (g_test_stall) a.flags = kPrefixTestStall;
 #endif
     // (all that can be refused comes before the first launch)
-    alignas(64) CUtensorMap tmk, tmv, tmq;
+    alignas(64) CUtensorMap tmk, tmv, tmv_last, tmq;
     if (S > 0) {
         if ((st = kernel_ready(pl.v.fn, pl.v.threads, pl.v.smem_bytes)) != KVD_OK) return st;
         if (pl.v.tma) {
-            const uint64_t dims[2] = {(uint64_t)D, (uint64_t)rows}, strides[1] = {(uint64_t)D * 2};
-            const uint32_t box[2] = {64, 64};
-            if ((st = encode_map_16bit(&tmk, k_prefix, dtype, 2, dims, strides, box)) != KVD_OK) return st;
-            if ((st = encode_map_16bit(&tmv, v_prefix, dtype, 2, dims, strides, box)) != KVD_OK) return st;
+            // (column, row, head, page) of the prefix; the rows end where it ends,
+            // so that TMA fills what lies past it with zeros
+            const uint64_t per_page = paged != nullptr ? (uint64_t)paged->page_size : (uint64_t)S_max;
+            const uint64_t strides[3] = {(uint64_t)D * 2, per_page * D * 2, per_page * D * 2 * H_kv};
+            const uint32_t box[4] = {64, 64, 1, 1};
+            uint64_t dims[4] = {(uint64_t)D, paged != nullptr ? per_page : (uint64_t)S, (uint64_t)H_kv,
+                                paged != nullptr ? (uint64_t)paged->num_pages : 1u};
+            if ((st = encode_map_16bit(&tmk, k_prefix, dtype, 4, dims, strides, box)) != KVD_OK) return st;
+            if ((st = encode_map_16bit(&tmv, v_prefix, dtype, 4, dims, strides, box)) != KVD_OK) return st;
+            if (paged != nullptr) dims[1] = (uint64_t)((S - 1) % paged->page_size + 1);
+            if ((st = encode_map_16bit(&tmv_last, v_prefix, dtype, 4, dims, strides, box)) != KVD_OK) return st;
             const uint64_t qdims[4] = {(uint64_t)D, (uint64_t)gN, (uint64_t)H_kv, (uint64_t)B};
             const uint64_t qstrides[3] = {(uint64_t)D * 2, (uint64_t)gN * D * 2, (uint64_t)H_kv * gN * D * 2};
             const uint32_t qbox[4] = {64, (uint32_t)std::min(gN, kPrefixBlock), 1, (uint32_t)pl.seqs};
@@ -149,7 +155,7 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
         cfg.gridDim = dim3((unsigned)pl.grid);
         cfg.blockDim = dim3((unsigned)pl.v.threads);
         cfg.dynamicSmemBytes = (size_t)pl.v.smem_bytes;
-        void *args[] = {&a, &tmk, &tmv, &tmq};
+        void *args[] = {&a, &tmk, &tmv, &tmv_last, &tmq};
         if (cudaLaunchKernelExC(&cfg, pl.v.fn, args) != cudaSuccess) return KVD_ERR_CUDA;
     }
     // 3. the join
@@ -166,7 +172,7 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     s.N = N;
     s.grid = pl.grid;
     cfg.gridDim = dim3((unsigned)(H_kv * pl.blocks * (kPrefixBlock / 32)), (unsigned)pl.v.join_grid_y);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     void *args[] = {&a, &s, &out};
     return cudaLaunchKernelExC(&cfg, pl.v.join_fn, args) == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;

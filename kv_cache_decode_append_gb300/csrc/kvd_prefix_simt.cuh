@@ -216,7 +216,7 @@ template <int D> void make_prefix_simt(bool paged, PrefixVariant *v)
     v->threads = PrefixSimtShape<D>::kThreads;
     v->smem_bytes = PrefixSimtShape<D>::kSmemBytes;
     v->tile_keys = PrefixSimtShape<D>::kTK;
-    v->join_grid_y = D / 4 / (4 * kJoinCols);
+    v->join_grid_y = D / 4 / (kJoinThreads / 32);
     v->tma = false;
 }
 

@@ -4,12 +4,13 @@
 // B), against key tiles of 128:
 //   * warp 8, the producer: Q blocks by a 4-D TMA box (64 columns x gN rows x 1
 //     head x seqs sequences: the box gathers the sequences' rows) at a piece's
-//     start; K and V tiles by 2-D TMA boxes of 64 keys x 128 bytes (a box never
-//     leaves a page) into a ring whose slots hold one K or one V tile each;
-//   * warp 9, the issuer: one thread issues S_X = Q_X . K^T (128 x 128 x D) and
-//     O_X += P_X . V (128 x D x 128) for X = A, B; before a last, partial tile's
-//     P . V the warp zeroes the value rows past the prefix (a zero weight times
-//     a stale NaN is NaN);
+//     start; K and V tiles by 4-D TMA boxes of 64 keys x 128 bytes (a box never
+//     leaves a page) into a ring whose slots hold one K or one V tile each.
+//     Value rows past the prefix must be zeros (a zero weight times a stale NaN
+//     is NaN): the maps end at the prefix (its last page has a map of its own),
+//     and TMA fills what lies outside a map with zeros;
+//   * warps 9 and 10, the issuers of A and B: one thread issues
+//     S_X = Q_X . K^T (128 x 128 x D) and O_X += P_X . V (128 x D x 128);
 //   * warps 0-3 and 4-7, the softmax warps of A and B: thread r owns row r
 //     (tensor-memory lane r): running max and sum in registers, weights P back
 //     into tensor memory as 16-bit pairs over the columns of S, O rescaled there
@@ -18,11 +19,15 @@
 // block's products.  Tensor memory: S_A, S_B of 128 columns (P_X over the first
 // 64 of S_X), O_A, O_B of D columns: all 512 for D = 128.
 //
-// S_X of the next tile overwrites P_X, so the issuer waits for P_X . V to
-// complete first (its commit on pv_done): it issues both blocks' P . V, then both
-// blocks' next S, so that the tensor core has work during that wait.  The O that
-// a softmax warp rescales is stable then: S_X(j) is issued after P_X . V(j - 1)
-// completed, and P_X . V(j) waits for the warp's own arrival.
+// A block's chain is S -> softmax -> P . V -> S of the next tile (which
+// overwrites P_X, so its issuer waits for P_X . V to complete first, by the
+// commit on pv_done): the first half of the keys' weights is handed over
+// (p_half) while the second is computed.  The O that a softmax warp rescales is
+// stable then: S_X(j) is issued after P_X . V(j - 1) completed, and P_X . V(j)
+// waits for the warp's own arrival.  An issuer per block, and one thread of it:
+// with one issuer for both, waiting for one block's P . V kept the other's
+// products back, and per-warp waits with shuffles cost hundreds of cycles each
+// (16384 keys, 8 KV heads of 512 rows: 49 us so, 36 with one thread).
 //
 // Every mbarrier is waited for phase by phase in order; every wait is bounded
 // and ends when another warp has given up; a CTA that gave up drains its copies
@@ -40,13 +45,13 @@ template <int D> struct PrefixTc5Shape {
     static constexpr int kBoxBytes = kTK * 128;         // one column box of a tile (or Q block)
     static constexpr int kTileBytes = kBoxes * kBoxBytes;
     static constexpr int kSlots = D == 128 ? 5 : 6;     // ring slots (a K or a V tile each)
-    static constexpr int kThreads = 320;
+    static constexpr int kThreads = 352;
     static constexpr int kTmemCols = 512;
     static constexpr int kTmemS = 0, kTmemO = 256;      // S_X at 128 X; O_X at 256 + D X
     static constexpr int kQOff = kSlots * kTileBytes;
     static constexpr int kBarOff = kQOff + 2 * kTileBytes;
-    // full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], p_full[2], pv_done[2], mma_done
-    static constexpr int kNumBars = 2 * kSlots + 9;
+    // full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], p_half[2], p_full[2], pv_done[2], mma_done[2]
+    static constexpr int kNumBars = 2 * kSlots + 12;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tensor-memory base, abort flag
     static constexpr int kSmemBytes = kMiscOff + 16;
     static_assert(D == 64 || D == 128, "head dim");
@@ -55,7 +60,8 @@ template <int D> struct PrefixTc5Shape {
     static_assert(2 * kSmemBytes > 227 * 1024, "one CTA per SM");
 };
 
-// 4-D tiled TMA load (see tma_load_2d).
+// 4-D tiled TMA load (see tma_load_2d), without an L2 policy: other CTAs read
+// the same tiles.
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint64_t *bar)
 {
     asm volatile(
@@ -64,20 +70,43 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, 
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
 }
-// 2-D tiled TMA load without an L2 policy: other CTAs read the same tile.
-__device__ __forceinline__ void tma_load_2d_shared(void *dst, const void *tmap, int x, int y, uint64_t *bar)
+// Bounded wait for phase `parity` of bar that also gives up once *abort is set;
+// the clock is read only once the phase is late.
+__device__ __forceinline__ bool prefix_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort)
 {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0u) {
+            if (*abort != 0u) return false;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kWaitLimitNs) return false;
+        }
+    }
+}
+
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar))
+        "{\n"
+        "  .reg .pred p;\n"
+        "  elect.sync _|p, 0xffffffff;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(r)
+        :
         : "memory");
+    return r != 0u;
 }
 
 template <typename T, int D, bool kPaged>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(352, 1)
     prefix_tc5_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q)
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v_last,
+                      const __grid_constant__ CUtensorMap tm_q)
 {
     using S = PrefixTc5Shape<D>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -88,7 +117,7 @@ __global__ void __launch_bounds__(320, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBarOff);
     uint64_t *empty = full + S::kSlots;
     uint64_t *q_full = empty + S::kSlots, *q_empty = q_full + 1;
-    uint64_t *s_full = q_full + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *mma_done = pv_done + 2;
+    uint64_t *s_full = q_full + 2, *p_half = s_full + 2, *p_full = p_half + 2, *pv_done = p_full + 2, *mma_done = pv_done + 2;
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + S::kMiscOff);
     volatile uint32_t *abort = misc + 1;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -102,16 +131,17 @@ __global__ void __launch_bounds__(320, 1)
     if (tid == 0) {
         for (int s = 0; s < S::kSlots; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);  // (both issuers)
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 128);
             mbar_init(&p_full[i], 128);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&mma_done[i], 1);
         }
-        mbar_init(mma_done, 1);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -139,34 +169,34 @@ __global__ void __launch_bounds__(320, 1)
             // the next ring slot, free
             auto take = [&]() -> int {
                 const int s = fills % S::kSlots;
-                if (fills >= S::kSlots && !tc5_wait(&empty[s], (uint32_t)(fills / S::kSlots - 1) & 1u, abort)) return -1;
+                if (fills >= S::kSlots && !prefix_wait(&empty[s], (uint32_t)(fills / S::kSlots - 1) & 1u, abort)) return -1;
                 ++fills;
                 return s;
             };
-            auto load_tile = [&](const CUtensorMap *map, int h, int tile, uint32_t extra) -> bool {
+            auto load_tile = [&](const CUtensorMap *map, const CUtensorMap *map_last, int h, int tile, uint32_t extra) -> bool {
                 const int s = take();
                 if (s < 0) return false;
                 unsigned char *dst = smem + s * S::kTileBytes;
                 mbar_arrive_expect_tx(&full[s], (uint32_t)S::kTileBytes + extra);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    // (a half past the prefix loads rows that are masked: the first half's again)
-                    int key = tile * S::kTK + half * 64;
-                    if (key >= a.S) key = tile * S::kTK;
-                    int y;
+                    const int key = tile * S::kTK + half * 64;
+                    int row = key, page = 0;  // (row: past the map's end where the half lies past the prefix)
+                    const CUtensorMap *m = map;
                     if constexpr (kPaged) {
-                        int page = __ldg(a.table + (key >> a.page_shift));
+                        const int last_page = (a.S - 1) >> a.page_shift;
+                        const int lp = min(key >> a.page_shift, last_page);
+                        row = key - (lp << a.page_shift);
+                        if (lp == last_page) m = map_last;
+                        page = __ldg(a.table + lp);
                         if ((unsigned)page >= (unsigned)a.num_pages) {  // never read outside the pool
                             raise_error(a.err_word, KVD_DEVERR_PAGE);
                             page = 0;
                         }
-                        y = ((page * a.H_kv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-                    } else {
-                        y = h * a.S_max + key;
                     }
 #pragma unroll
                     for (int bx = 0; bx < S::kBoxes; ++bx)
-                        tma_load_2d_shared(dst + bx * S::kBoxBytes + half * 64 * 128, map, bx * 64, y, &full[s]);
+                        tma_load_4d(dst + bx * S::kBoxBytes + half * 64 * 128, m, bx * 64, row, h, page, &full[s]);
                 }
                 return true;
             };
@@ -174,7 +204,7 @@ __global__ void __launch_bounds__(320, 1)
             for (int t = lo; t < hi && !dead; ++t) {
                 const int h = u / a.units_per_head;
                 if (t == lo || k == 0) {  // a piece starts: its Q blocks
-                    if (q_loads > 0 && !tc5_wait(q_empty, (uint32_t)(q_loads - 1) & 1u, abort)) {
+                    if (q_loads > 0 && !prefix_wait(q_empty, (uint32_t)(q_loads - 1) & 1u, abort)) {
                         dead = true;
                         break;
                     }
@@ -195,7 +225,7 @@ __global__ void __launch_bounds__(320, 1)
 #ifdef KVD_TIMEOUT_TEST
                 if ((a.flags & kPrefixTestStall) && t == lo) extra = 16u;  // a stage that never completes
 #endif
-                dead = !load_tile(&tm_k, h, k, extra) || !load_tile(&tm_v, h, k, 0u);
+                dead = !load_tile(&tm_k, &tm_k, h, k, extra) || !load_tile(&tm_v, &tm_v_last, h, k, 0u);
                 if (++k == a.n_tiles) {
                     k = 0;
                     ++u;
@@ -216,113 +246,106 @@ __global__ void __launch_bounds__(320, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 9) {
-        // ---- issuer ----
-        constexpr uint32_t kIdescS = tc5_idesc<kBf16>(128, S::kTK, false, false);
-        constexpr uint32_t kIdescO = tc5_idesc<kBf16>(128, D, false, true);
-        const uint32_t ring = smem_addr(smem), qbuf = smem_addr(smem + S::kQOff);
-        bool dead = false;
-        // waits by lane 0, decided for the warp
-        auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-            int ok = 1;
-            if (lane == 0) ok = tc5_wait(bar, parity & 1u, abort) ? 1 : 0;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) dead = true;
-            return ok != 0;
-        };
-        auto issue_s = [&](int x, uint32_t kt) {
-            if (lane == 0) {
-                tc5_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc5_mma_f16(tmem + S::kTmemS + x * 128,
-                                tc5_desc(qbuf + x * S::kTileBytes + (ks >> 2) * S::kBoxBytes + (ks & 3) * 32, 0u, 1024u),
-                                tc5_desc(kt + (ks >> 2) * S::kBoxBytes + (ks & 3) * 32, 0u, 1024u), kIdescS,
-                                ks > 0 ? 1u : 0u);
+    } else if (warp >= 9) {
+        // ---- issuer of block x: one thread ----
+        const int x = warp - 9;
+        if (elect_one()) {
+            constexpr uint32_t kIdescS = tc5_idesc<kBf16>(128, S::kTK, false, false);
+            constexpr uint32_t kIdescO = tc5_idesc<kBf16>(128, D, false, true);
+            // (a descriptor's address field counts 16 bytes; slots and k-steps add to it)
+            const uint64_t desc_q = tc5_desc(smem_addr(smem + S::kQOff + x * S::kTileBytes), 0u, 1024u);
+            const uint64_t desc_k = tc5_desc(smem_addr(smem), 0u, 1024u);
+            const uint64_t desc_v = tc5_desc(smem_addr(smem), (uint32_t)S::kBoxBytes, 1024u);
+            const uint32_t t_s = tmem + S::kTmemS + x * 128, t_o = tmem + S::kTmemO + x * D;
+            bool ok = true;
+            auto issue_s = [&](int slot) {
+                const uint64_t kd = desc_k + slot * (S::kTileBytes / 16);
+#pragma unroll 1
+                for (int ks = 0; ks < D / 16; ++ks) {  // (rolled: the tensor core sets the pace, and code this
+                                                       // warp runs rarely should be short)
+                    const int step = ((ks >> 2) * S::kBoxBytes + (ks & 3) * 32) / 16;
+                    tc5_mma_f16(t_s, desc_q + step, kd + step, kIdescS, ks > 0 ? 1u : 0u);
+                }
                 tc5_commit(&s_full[x]);
-            }
-        };
-        auto issue_pv = [&](int x, uint32_t vt, bool first) {
-            if (lane == 0) {
-                tc5_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < S::kTK / 16; ++ks)
-                    tc5_mma_f16_ts(tmem + S::kTmemO + x * D, tmem + S::kTmemS + x * 128 + ks * 8,
-                                   tc5_desc(vt + ks * 16 * 128, (uint32_t)S::kBoxBytes, 1024u), kIdescO,
-                                   (ks > 0 || !first) ? 1u : 0u);
-                tc5_commit(&pv_done[x]);
-            }
-        };
-        int u = u_lo, k = k_lo, f = 0;  // f: ring fills consumed (K of this tile is fill f)
-        int pieces = 0;
-        uint32_t n_s[2] = {0u, 0u};     // tiles of each block so far (phases of its barriers)
-        bool have_s = false;            // S of tile t is issued already
-        for (int t = lo; t < hi && !dead; ++t) {
-            const int nb = min(a.unit_blocks, a.blocks - (u % a.units_per_head) * a.unit_blocks);
-            const bool first = t == lo || k == 0;
-            const bool last = t == hi - 1 || k == a.n_tiles - 1;
-            if (!have_s) {
-                if (!wait(q_full, (uint32_t)pieces)) break;
-                ++pieces;
-                if (!wait(&full[f % S::kSlots], (uint32_t)(f / S::kSlots))) break;
-                // (S_X lies over the previous piece's last P_X)
-                for (int x = 0; x < nb && !dead; ++x)
-                    if (n_s[x] > 0u) wait(&pv_done[x], n_s[x] - 1u);
-                if (dead) break;
-                for (int x = 0; x < nb; ++x) issue_s(x, ring + (f % S::kSlots) * S::kTileBytes);
-                if (lane == 0) {
-                    tc5_commit(&empty[f % S::kSlots]);
-                    if (last) tc5_commit(q_empty);
+                tc5_commit(&empty[slot]);
+            };
+            auto issue_pv = [&](int slot, int half, bool first) {
+                const uint64_t vd = desc_v + slot * (S::kTileBytes / 16);
+#pragma unroll 1
+                for (int i = 0; i < S::kTK / 32; ++i) {
+                    const int ks = half * (S::kTK / 32) + i;
+                    tc5_mma_f16_ts(t_o, t_s + ks * 8, vd + ks * (16 * 128 / 16), kIdescO, (ks > 0 || !first) ? 1u : 0u);
+                }
+            };
+            // the ring's next fill (K and V of each tile in turn), as slot and parity
+            int slot = 0;
+            uint32_t par = 0u;
+            auto step = [&]() {
+                if (++slot == S::kSlots) {
+                    slot = 0;
+                    par ^= 1u;
+                }
+            };
+            int u = u_lo, k = k_lo;
+            uint32_t pieces = 0u, n = 0u;  // pieces, and tiles of this block, so far
+            bool have_s = false;           // S of tile t is issued already
+            for (int t = lo; t < hi; ++t) {
+                const bool mine = (u % a.units_per_head) * a.unit_blocks + x < a.blocks && x < a.unit_blocks;
+                const bool first = t == lo || k == 0;
+                const bool last = t == hi - 1 || k == a.n_tiles - 1;
+                if (first) {
+                    ok = prefix_wait(q_full, pieces & 1u, abort);
+                    ++pieces;
+                    if (!ok) break;
+                }
+                if (!mine) {  // (a unit of one block: the slots pass by)
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        ok = prefix_wait(&full[slot], par, abort);
+                        if (ok) mbar_arrive(&empty[slot]);
+                        step();
+                    }
+                    if (!ok) break;
+                    if (last) mbar_arrive(q_empty);
+                } else {
+                    if (!have_s) {
+                        // (S_X lies over the previous piece's last P_X)
+                        ok = prefix_wait(&full[slot], par, abort) && (n == 0u || prefix_wait(&pv_done[x], (n - 1u) & 1u, abort));
+                        if (!ok) break;
+                        tc5_fence_after();
+                        issue_s(slot);
+                        if (last) tc5_commit(q_empty);
+                        step();
+                    }
+                    const int vs = slot;
+                    if (!(ok = prefix_wait(&full[vs], par, abort) && prefix_wait(&p_half[x], n & 1u, abort))) break;
+                    step();
+                    tc5_fence_after();
+                    issue_pv(vs, 0, first);
+                    if (!(ok = prefix_wait(&p_full[x], n & 1u, abort))) break;
+                    tc5_fence_after();
+                    issue_pv(vs, 1, first);
+                    tc5_commit(&pv_done[x]);
+                    tc5_commit(&empty[vs]);
+                    if (!last) {  // the next tile's S once this P . V is complete
+                        if (!(ok = prefix_wait(&full[slot], par, abort) && prefix_wait(&pv_done[x], n & 1u, abort))) break;
+                        issue_s(slot);
+                        if (t + 1 == hi - 1 || k + 1 == a.n_tiles - 1) tc5_commit(q_empty);
+                        step();
+                    }
+                    have_s = !last;
+                    ++n;
+                }
+                if (++k == a.n_tiles) {
+                    k = 0;
+                    ++u;
                 }
             }
-            const int fv = f + 1, sv = fv % S::kSlots;
-            if (!wait(&full[sv], (uint32_t)(fv / S::kSlots))) break;
-            const uint32_t vt = ring + sv * S::kTileBytes;
-            const int nk = a.S - k * S::kTK;
-            if (nk < S::kTK) {  // value rows past the prefix: zero
-                for (int idx = lane; idx < (S::kTK - nk) * (D / 8); idx += 32) {
-                    const int r = nk + idx / (D / 8), c = idx % (D / 8);
-                    const uint32_t lin = vt + (c >> 3) * S::kBoxBytes + r * 128 + ((c & 7) << 4);
-                    sts128(lin ^ ((lin >> 3) & 0x70u), make_uint4(0u, 0u, 0u, 0u));
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-            }
-            for (int x = 0; x < nb && !dead; ++x) {
-                if (!wait(&p_full[x], n_s[x])) break;
-                issue_pv(x, vt, first);
-            }
-            if (dead) break;
-            if (lane == 0) tc5_commit(&empty[sv]);
-            have_s = !last;
-            if (!last) {  // the next tile's S, each block's once its P . V is complete
-                const int fk = f + 2, sk = fk % S::kSlots;
-                if (!wait(&full[sk], (uint32_t)(fk / S::kSlots))) break;
-                const bool next_last = t + 1 == hi - 1 || k + 1 == a.n_tiles - 1;
-                for (int x = 0; x < nb && !dead; ++x) {
-                    if (!wait(&pv_done[x], n_s[x])) break;
-                    issue_s(x, ring + sk * S::kTileBytes);
-                }
-                if (dead) break;
-                if (lane == 0) {
-                    tc5_commit(&empty[sk]);
-                    if (next_last) tc5_commit(q_empty);
-                }
-            }
-            for (int x = 0; x < nb; ++x) ++n_s[x];
-            f += 2;
-            if (++k == a.n_tiles) {
-                k = 0;
-                ++u;
-            }
-        }
-        if (lane == 0) {
-            if (dead) {
+            if (!ok) {
                 *abort = 1u;
                 raise_error(a.err_word, KVD_DEVERR_TIMEOUT);
             }
-            tc5_commit(mma_done);  // this thread's products complete before the tensor memory is freed
-            mbar_wait_drain(mma_done, 0u);
+            tc5_commit(&mma_done[x]);  // this thread's products complete before the tensor memory is freed
+            mbar_wait_drain(&mma_done[x], 0u);
         }
         __syncwarp();
     } else {
@@ -334,14 +357,14 @@ __global__ void __launch_bounds__(320, 1)
         uint32_t n_s = 0u;
         bool dead = false;
         auto warp_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, tc5_wait(bar, parity & 1u, abort));
+            return __all_sync(0xffffffffu, prefix_wait(bar, parity & 1u, abort));
         };
         int u = u_lo, k = k_lo;
         for (int t = lo; t < hi; ++t) {
             const int b0 = (u % a.units_per_head) * a.unit_blocks;
             const bool first = t == lo || k == 0;
             const bool last = t == hi - 1 || k == a.n_tiles - 1;
-            if (b0 + x < a.blocks) {
+            if (b0 + x < a.blocks && x < a.unit_blocks) {
                 if (first) {
                     m_run = kNegInf;
                     l_run = 0.f;
@@ -362,13 +385,11 @@ __global__ void __launch_bounds__(320, 1)
                         if (64 + c >= nk) s1[c] = 0xff800000u;
                     }
                 }
-                float mx[8];
+                // (four chains of three-input maxima)
+                float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mx[i] = fmaxf(__uint_as_float(s0[i]), __uint_as_float(s1[i]));
-#pragma unroll
-                for (int c = 8; c < 64; ++c) mx[c & 7] = fmaxf(mx[c & 7], fmaxf(__uint_as_float(s0[c]), __uint_as_float(s1[c])));
-                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * a.qscale;
+                for (int c = 0; c < 64; ++c) mx[c & 3] = max3(mx[c & 3], __uint_as_float(s0[c]), __uint_as_float(s1[c]));
+                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.qscale;
                 float alpha = 1.f;
                 bool rescale = false;
                 if (top > m_run + kRescaleThreshold) {
@@ -388,28 +409,31 @@ __global__ void __launch_bounds__(320, 1)
                         tc5_st32(t_o + c0, o);
                     }
                 }
+                // weights 2^(qscale s - m): scale and maximum in one packed FMA,
+                // sums as packed pairs in four chains
                 const float nmu = (m_run == kNegInf) ? 0.f : -m_run;
-                float l8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) l8[i] = 0.f;
+                const f32x2 q2 = pack2(a.qscale, a.qscale), nmu2 = pack2(nmu, nmu);
+                f32x2 l4[4] = {0ull, 0ull, 0ull, 0ull};
                 uint32_t pk[32];
+                auto weights = [&](const uint32_t (&s)[64]) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float p0 = fast_exp2(fmaf(__uint_as_float(s0[2 * c]), a.qscale, nmu));
-                    const float p1 = fast_exp2(fmaf(__uint_as_float(s0[2 * c + 1]), a.qscale, nmu));
-                    l8[c & 7] += p0 + p1;
-                    pk[c] = pack_pair<T>(p0, p1);
-                }
+                    for (int c = 0; c < 32; ++c) {
+                        float y0, y1;
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), q2, nmu2), y0, y1);
+                        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                        l4[c & 3] = add2(l4[c & 3], pack2(p0, p1));
+                        pk[c] = pack_pair<T>(p0, p1);
+                    }
+                };
+                weights(s0);
                 tc5_st32(t_s, pk);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float p0 = fast_exp2(fmaf(__uint_as_float(s1[2 * c]), a.qscale, nmu));
-                    const float p1 = fast_exp2(fmaf(__uint_as_float(s1[2 * c + 1]), a.qscale, nmu));
-                    l8[c & 7] += p0 + p1;
-                    pk[c] = pack_pair<T>(p0, p1);
-                }
+                tc5_fence_before();
+                mbar_arrive(&p_half[x]);
+                weights(s1);
                 tc5_st32(t_s + 32, pk);
-                l_run = l_run * alpha + (((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7])));
+                float le, lo2;
+                unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), le, lo2);
+                l_run = l_run * alpha + (le + lo2);
                 tc5_fence_before();
                 mbar_arrive(&p_full[x]);
                 if (last) {
@@ -477,7 +501,7 @@ template <typename T> bool pick_prefix_tc5(int D, bool paged, PrefixVariant *v)
     }
     v->threads = PrefixTc5Shape<128>::kThreads;
     v->tile_keys = PrefixTc5Shape<128>::kTK;
-    v->join_grid_y = D / 4 / (4 * kJoinCols);
+    v->join_grid_y = D / 4 / (kJoinThreads / 32);
     v->tma = true;
     return true;
 }

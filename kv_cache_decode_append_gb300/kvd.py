@@ -1,7 +1,9 @@
 """Thin ctypes binding of ``include/kvd.h``.
 
 Argument marshalling only: every step of the decode path runs in the CUDA
-kernels of ``libkvd.so``.  There is no fallback: when the library is missing
+kernels of ``libkvd.so``.  The calls added for whole serving steps (rotated
+append, scored attention, shared prefixes) marshal in a compiled extension
+module linked against it.  There is no fallback: when the library is missing
 or a call returns a non-OK status, these functions raise.
 
 Two layers, same names as the C ABI:
@@ -15,6 +17,7 @@ Two layers, same names as the C ABI:
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -593,82 +596,33 @@ def kvd_decode_step_e4m3(q, k_cache, v_cache, k_new, v_new, out, past_len, max_p
 
 
 # ---------------------------------------------------------------------------------
+# The calls below are checked and marshalled by the extension module of
+# csrc/kvd_binding.cpp (dtype, device, contiguity, shapes: ValueError).
+_calls = None
+
+
+def _compiled():
+    """The extension module of the compiled calls; raises if it has not been built."""
+    global _calls
+    if _calls is None:
+        load()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        spec = importlib.util.spec_from_file_location("_kvd", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _calls = module
+    return _calls
+
+
+def _handle(stream):
+    return stream if stream is None else _stream_handle(stream)
+
+
+# ---------------------------------------------------------------------------------
 # rotated append
-def _ready(t, dtype, dev: int) -> bool:
-    """A contiguous CUDA tensor of this dtype on this device."""
-    return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
-            and t.get_device() == dev)
-
-
-def _refuse(dev: int, *named) -> None:
-    """Raise for the first of (name, tensor, dtype) that is not _ready on the current device."""
-    for n, t, dt in named:
-        if t is not None:
-            _need_cuda(n, t, dt)
-            if t.get_device() != dev:
-                raise ValueError(f"{n} must be on the current CUDA device (cuda:{dev}), got {t.device}")
-
-
-def _need_ready(*named) -> None:
-    """Every (name, tensor, dtype), None skipped, is a contiguous CUDA tensor of its dtype on the current
-    device, where the library launches."""
-    dev = torch.cuda.current_device()
-    for n, t, dt in named:
-        if t is not None and not _ready(t, dt, dev):
-            _refuse(dev, (n, t, dt))
-
-
-def _need_rows(name: str, t: torch.Tensor, dtype) -> None:
-    """[B, H, N, D] rows on the current device: each row contiguous, the rows at any non-negative strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
-        raise ValueError(f"{name} must be [B, H, N, D] with contiguous rows")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-
-
-def _rope_rows(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, pos_base, positions, err_word):
-    """Checks common to the rotated appends; returns (B, H_q, H_kv, N, D, strides or None)."""
-    dt = k_cache.dtype
-    dev = torch.cuda.current_device()
-    dense = _ready(q, dt, dev) and _ready(k_new, dt, dev) and _ready(v_new, dt, dev)
-    if not dense or q.dim() != 4:
-        for n, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
-            _need_rows(n, t, dt)
-    if not (_ready(q_out, dt, dev) and _ready(k_cache, dt, dev) and _ready(v_cache, dt, dev)
-            and _ready(past_len, torch.int32, dev) and _ready(inv_freq, torch.float64, dev)):
-        _refuse(dev, ("q_out", q_out, dt), ("k_cache", k_cache, dt), ("v_cache", v_cache, dt),
-                ("past_len", past_len, torch.int32), ("inv_freq", inv_freq, torch.float64))
-    B, H_q, N, D = q.shape
-    new = k_new.shape
-    H_kv = new[1]
-    if positions is not None:
-        _need_ready(("positions", positions, torch.int32))
-        if tuple(positions.shape) != (B, N):
-            raise ValueError("positions must be [B, N]")
-    if err_word is not None:
-        _need_ready(("err_word", err_word, torch.int32))
-    if new != (B, H_kv, N, D) or v_new.shape != new or q_out.shape != q.shape:
-        raise ValueError("shape mismatch between q, q_out and the new K/V")
-    cache = k_cache.shape
-    if v_cache.shape != cache or len(cache) != 4 or cache[1] != H_kv or cache[3] != D:
-        raise ValueError("shape mismatch between the caches and the new K/V")
-    if past_len.numel() != B:
-        raise ValueError("past_len must hold B entries")
-    if not -(1 << 31) <= pos_base < 1 << 31:
-        raise ValueError("pos_base must fit in 32 bits")
-    if dense:
-        return B, H_q, H_kv, N, D, None
-    if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
-        raise ValueError("q_out may be q only when q is contiguous")
-    # (a dimension of one row has no stride that matters; torch may report any)
-    st = [s if n > 1 else 0 for t in (q, k_new, v_new) for s, n in zip(t.stride()[:3], t.shape[:3])]
-    return B, H_q, H_kv, N, D, (ctypes.c_int64 * 9)(*st)
-
-
 def kvd_rope_append(q, q_out, k_cache, v_cache, k_new, v_new, past_len, max_past_len: int, inv_freq,
                     interleaved: bool = False, pos_base: int = 0, positions=None, err_word=None,
                     stream=None) -> None:
@@ -680,33 +634,20 @@ def kvd_rope_append(q, q_out, k_cache, v_cache, k_new, v_new, past_len, max_past
     is ``pos_base + positions[b, i]``, without ``positions`` ``pos_base + past_len[b] + i``.  ``q``,
     ``k_new`` and ``v_new`` may be strided views with contiguous rows (the parts of a fused
     projection); ``q_out`` may be ``q``."""
-    B, H_q, H_kv, N, D, strides = _rope_rows(q, q_out, k_new, v_new, k_cache, v_cache, past_len, inv_freq, pos_base,
-                                             positions, err_word)
-    if k_cache.shape[0] != B:
-        raise ValueError("shape mismatch between the caches and the new K/V")
-    st = raw.kvd_rope_append(q.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
-                             v_new.data_ptr(), strides, past_len.data_ptr(), _ptr(positions), int(pos_base),
-                             inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), B, H_q, H_kv,
-                             k_cache.shape[2], D, N, int(max_past_len), _dtype_code(k_cache), _ptr(err_word),
-                             _stream_handle(stream))
-    _check("kvd_rope_append", st)
+    st = _compiled().rope_append(q, q_out, k_cache, v_cache, k_new, v_new, past_len, max_past_len, inv_freq, interleaved,
+                                 pos_base, positions, err_word, _handle(stream))
+    if st:
+        raise KvdError("kvd_rope_append", st)
 
 
 def kvd_paged_rope_append(q, q_out, k_pages, v_pages, k_new, v_new, block_table, past_len, max_past_len: int, inv_freq,
                           interleaved: bool = False, pos_base: int = 0, positions=None, err_word=None,
                           stream=None) -> None:
     """kvd_rope_append into the page slots of tokens ``past_len[b] + i``."""
-    B, H_q, H_kv, N, D, strides = _rope_rows(q, q_out, k_new, v_new, k_pages, v_pages, past_len, inv_freq, pos_base,
-                                             positions, err_word)
-    num_pages, _, page_size, _, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
-    _need_ready(("block_table", block_table, torch.int32))
-    st = raw.kvd_paged_rope_append(q.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                   k_new.data_ptr(), v_new.data_ptr(), strides, block_table.data_ptr(),
-                                   past_len.data_ptr(), _ptr(positions), int(pos_base), inv_freq.data_ptr(),
-                                   2 * inv_freq.numel(), int(interleaved), B, H_q, H_kv, D, N, page_size, max_pages,
-                                   num_pages, int(max_past_len), _dtype_code(k_pages), _ptr(err_word),
-                                   _stream_handle(stream))
-    _check("kvd_paged_rope_append", st)
+    st = _compiled().paged_rope_append(q, q_out, k_pages, v_pages, k_new, v_new, block_table, past_len, max_past_len,
+                                       inv_freq, interleaved, pos_base, positions, err_word, _handle(stream))
+    if st:
+        raise KvdError("kvd_paged_rope_append", st)
 
 
 # ---------------------------------------------------------------------------------
@@ -720,19 +661,6 @@ def alloc_scored_workspace(B, H_q, H_kv, D, N, max_past_len, dtype, device=None)
     return torch.zeros(n, dtype=torch.uint8, device=device or torch.device("cuda"))
 
 
-def _score(q, softcap, slopes, window, doc_start, prefix_len) -> Score:
-    B, H_q, N, _ = q.shape
-    for n, t, dt, shape in (("slopes", slopes, torch.float32, (H_q,)), ("doc_start", doc_start, torch.int32, (B, N)),
-                            ("prefix_len", prefix_len, torch.int32, (B,))):
-        if t is not None:
-            _need_ready((n, t, dt))
-            if t.shape != shape:
-                raise ValueError(f"{n} must be {list(shape)}")
-    if not 0 <= window < 1 << 31:
-        raise ValueError("window must be at least 0 and fit in 32 bits")
-    return Score(float(softcap), _ptr(slopes), int(window), _ptr(doc_start), _ptr(prefix_len))
-
-
 def kvd_decode_attention_scored(q, k_cache, v_cache, out, past_len, max_past_len: int, softcap: float = 0.0,
                                 slopes=None, window: int = 0, doc_start=None, prefix_len=None, scale: float = 0.0,
                                 workspace: Optional[torch.Tensor] = None, err_word=None, stream=None) -> None:
@@ -743,22 +671,10 @@ def kvd_decode_attention_scored(q, k_cache, v_cache, out, past_len, max_past_len
     the last ``window`` keys up to its own; ``prefix_len`` int32 [B]: the first keys, seen by every row;
     ``doc_start`` int32 [B, N]: a row sees no key before its document's first.  A row that sees no key
     gets zeros.  Workspace: ``alloc_scored_workspace``."""
-    dt = q.dtype
-    _need_ready(("q", q, dt), ("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("out", out, dt),
-                ("past_len", past_len, torch.int32), ("workspace", workspace, torch.uint8), ("err_word", err_word, torch.int32))
-    B, H_q, N, D = q.shape
-    _, H_kv, T_max, _ = k_cache.shape
-    if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
-        raise ValueError("shape mismatch between q, out and the caches")
-    if past_len.numel() != B:
-        raise ValueError("past_len must hold B entries")
-    score = _score(q, softcap, slopes, window, doc_start, prefix_len)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = raw.kvd_decode_attention_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
-                                         past_len.data_ptr(), ctypes.byref(score), B, H_q, H_kv, T_max, D, N,
-                                         int(max_past_len), float(scale), _dtype_code(q), ws_ptr, ws_bytes,
-                                         _ptr(err_word), _stream_handle(stream))
-    _check("kvd_decode_attention_scored", st)
+    st = _compiled().decode_attention_scored(q, k_cache, v_cache, out, past_len, max_past_len, softcap, slopes, window,
+                                             doc_start, prefix_len, scale, workspace, err_word, _handle(stream))
+    if st:
+        raise KvdError("kvd_decode_attention_scored", st)
 
 
 def kvd_paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, past_len, max_past_len: int,
@@ -766,24 +682,11 @@ def kvd_paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, pas
                                       prefix_len=None, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
                                       err_word=None, stream=None) -> None:
     """kvd_decode_attention_scored over a paged cache; pages that hold only keys no row sees are not read."""
-    dt = q.dtype
-    _need_ready(("q", q, dt), ("k_pages", k_pages, dt), ("v_pages", v_pages, dt), ("out", out, dt),
-                ("block_table", block_table, torch.int32), ("past_len", past_len, torch.int32),
-                ("workspace", workspace, torch.uint8), ("err_word", err_word, torch.int32))
-    B, H_q, N, D = q.shape
-    num_pages, H_kv, page_size, Dp, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
-    if out.shape != q.shape or Dp != D:
-        raise ValueError("shape mismatch between q, out and the pages")
-    if past_len.numel() != B:
-        raise ValueError("past_len must hold B entries")
-    score = _score(q, softcap, slopes, window, doc_start, prefix_len)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = raw.kvd_paged_decode_attention_scored(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
-                                               block_table.data_ptr(), past_len.data_ptr(), ctypes.byref(score), B,
-                                               H_q, H_kv, D, N, page_size, max_pages, num_pages, int(max_past_len),
-                                               float(scale), _dtype_code(q), ws_ptr, ws_bytes, _ptr(err_word),
-                                               _stream_handle(stream))
-    _check("kvd_paged_decode_attention_scored", st)
+    st = _compiled().paged_decode_attention_scored(q, k_pages, v_pages, out, block_table, past_len, max_past_len, softcap,
+                                                   slopes, window, doc_start, prefix_len, scale, workspace, err_word,
+                                                   _handle(stream))
+    if st:
+        raise KvdError("kvd_paged_decode_attention_scored", st)
 
 
 # ---------------------------------------------------------------------------------
@@ -804,51 +707,20 @@ def kvd_shared_prefix_attention(q, k_prefix, v_prefix, prefix_len: int, k_cache,
     """kvd_decode_attention of sequences that share their first ``prefix_len`` tokens: ``k_prefix`` and
     ``v_prefix`` [H_kv, S_max, D] hold them once, the caches [B, H_kv, T_max, D] and ``past_len`` only what
     follows.  Workspace: ``alloc_shared_prefix_workspace``."""
-    dt = q.dtype
-    _need_ready(("q", q, dt), ("k_prefix", k_prefix, dt), ("v_prefix", v_prefix, dt), ("k_cache", k_cache, dt),
-                ("v_cache", v_cache, dt), ("out", out, dt), ("past_len", past_len, torch.int32),
-                ("workspace", workspace, torch.uint8), ("err_word", err_word, torch.int32))
-    B, H_q, N, D = q.shape
-    _, H_kv, T_max, _ = k_cache.shape
-    if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
-        raise ValueError("shape mismatch between q, out and the caches")
-    if k_prefix.dim() != 3 or v_prefix.shape != k_prefix.shape or k_prefix.shape[0] != H_kv or k_prefix.shape[2] != D:
-        raise ValueError("k_prefix and v_prefix must be the same [H_kv, S_max, D]")
-    if past_len.numel() != B:
-        raise ValueError("past_len must hold B entries")
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = raw.kvd_shared_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
-                                         v_cache.data_ptr(), out.data_ptr(), past_len.data_ptr(), B, H_q, H_kv,
-                                         k_prefix.shape[1], T_max, D, N, int(prefix_len), int(max_past_len),
-                                         float(scale), _dtype_code(q), ws_ptr, ws_bytes, _ptr(err_word),
-                                         _stream_handle(stream))
-    _check("kvd_shared_prefix_attention", st)
+    st = _compiled().shared_prefix_attention(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, out, past_len,
+                                             max_past_len, scale, workspace, err_word, _handle(stream))
+    if st:
+        raise KvdError("kvd_shared_prefix_attention", st)
 
 
 def kvd_paged_shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len: int, out, block_table, past_len,
                                       max_past_len: int, scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
                                       err_word=None, stream=None) -> None:
     """kvd_shared_prefix_attention over a page pool: ``prefix_table`` int32 names the prefix's pages."""
-    dt = q.dtype
-    _need_ready(("q", q, dt), ("k_pages", k_pages, dt), ("v_pages", v_pages, dt), ("out", out, dt),
-                ("prefix_table", prefix_table, torch.int32), ("block_table", block_table, torch.int32),
-                ("past_len", past_len, torch.int32), ("workspace", workspace, torch.uint8),
-                ("err_word", err_word, torch.int32))
-    B, H_q, N, D = q.shape
-    num_pages, H_kv, page_size, Dp, max_pages = _paged_geometry(k_pages, v_pages, block_table, B)
-    if out.shape != q.shape or Dp != D:
-        raise ValueError("shape mismatch between q, out and the pages")
-    if past_len.numel() != B:
-        raise ValueError("past_len must hold B entries")
-    if prefix_table.numel() * page_size < prefix_len:
-        raise ValueError("prefix_table must name every page of the prefix")
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = raw.kvd_paged_shared_prefix_attention(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
-                                               prefix_table.data_ptr(), block_table.data_ptr(), past_len.data_ptr(), B,
-                                               H_q, H_kv, D, N, page_size, max_pages, num_pages, int(prefix_len),
-                                               int(max_past_len), float(scale), _dtype_code(q), ws_ptr, ws_bytes,
-                                               _ptr(err_word), _stream_handle(stream))
-    _check("kvd_paged_shared_prefix_attention", st)
+    st = _compiled().paged_shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, out, block_table,
+                                                   past_len, max_past_len, scale, workspace, err_word, _handle(stream))
+    if st:
+        raise KvdError("kvd_paged_shared_prefix_attention", st)
 
 
 def kvd_decode_attention_noalloc(q, k_cache, v_cache, out, past_len, max_past_len: int,

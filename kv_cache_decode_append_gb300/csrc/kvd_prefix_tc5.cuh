@@ -9,8 +9,8 @@
 //     Value rows past the prefix must be zeros (a zero weight times a stale NaN
 //     is NaN): the maps end at the prefix (its last page has a map of its own),
 //     and TMA fills what lies outside a map with zeros;
-//   * warps 9 and 10, the issuers of A and B: one thread issues
-//     S_X = Q_X . K^T (128 x 128 x D) and O_X += P_X . V (128 x D x 128);
+//   * warp 9, the issuer: one thread issues S_X = Q_X . K^T (128 x 128 x D) and
+//     O_X += P_X . V (128 x D x 128) for X = A, B;
 //   * warps 0-3 and 4-7, the softmax warps of A and B: thread r owns row r
 //     (tensor-memory lane r): running max and sum in registers, weights P back
 //     into tensor memory as 16-bit pairs over the columns of S, O rescaled there
@@ -19,15 +19,17 @@
 // block's products.  Tensor memory: S_A, S_B of 128 columns (P_X over the first
 // 64 of S_X), O_A, O_B of D columns: all 512 for D = 128.
 //
-// A block's chain is S -> softmax -> P . V -> S of the next tile (which
-// overwrites P_X, so its issuer waits for P_X . V to complete first, by the
-// commit on pv_done): the first half of the keys' weights is handed over
-// (p_half) while the second is computed.  The O that a softmax warp rescales is
-// stable then: S_X(j) is issued after P_X . V(j - 1) completed, and P_X . V(j)
-// waits for the warp's own arrival.  An issuer per block, and one thread of it:
-// with one issuer for both, waiting for one block's P . V kept the other's
-// products back, and per-warp waits with shuffles cost hundreds of cycles each
-// (16384 keys, 8 KV heads of 512 rows: 49 us so, 36 with one thread).
+// A block's chain is S -> softmax -> P . V -> S of the next tile, which
+// overwrites P_X: the issuer waits for P_X . V to complete first (its commit on
+// pv_done).  The O that a softmax warp rescales is stable then: S_X(j) is issued
+// after P_X . V(j - 1) completed, and P_X . V(j) waits for the warp's arrival.
+// What bounds the loop is shared memory: S reads 8 KB of operands per 64 cycles
+// of the tensor core, all that shared memory delivers, P . V half, TMA writes the
+// tiles; a barrier tested meanwhile takes 100 cycles and more.  So the issuer is
+// one thread that blocks on the barriers in their expected order.  Measured at
+// 16384 keys, 8 KV heads of 512 rows: 36 us so; 39 us with an issuer per block
+// (their products take turns and both come late), 40 us with one that tests
+// both blocks' barriers in turn, 49 us with whole-warp waits.
 //
 // Every mbarrier is waited for phase by phase in order; every wait is bounded
 // and ends when another warp has given up; a CTA that gave up drains its copies
@@ -45,13 +47,13 @@ template <int D> struct PrefixTc5Shape {
     static constexpr int kBoxBytes = kTK * 128;         // one column box of a tile (or Q block)
     static constexpr int kTileBytes = kBoxes * kBoxBytes;
     static constexpr int kSlots = D == 128 ? 5 : 6;     // ring slots (a K or a V tile each)
-    static constexpr int kThreads = 352;
+    static constexpr int kThreads = 320;
     static constexpr int kTmemCols = 512;
     static constexpr int kTmemS = 0, kTmemO = 256;      // S_X at 128 X; O_X at 256 + D X
     static constexpr int kQOff = kSlots * kTileBytes;
     static constexpr int kBarOff = kQOff + 2 * kTileBytes;
-    // full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], p_half[2], p_full[2], pv_done[2], mma_done[2]
-    static constexpr int kNumBars = 2 * kSlots + 12;
+    // full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], p_full[2], pv_done[2], mma_done
+    static constexpr int kNumBars = 2 * kSlots + 9;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tensor-memory base, abort flag
     static constexpr int kSmemBytes = kMiscOff + 16;
     static_assert(D == 64 || D == 128, "head dim");
@@ -103,7 +105,7 @@ __device__ __forceinline__ bool elect_one()
 }
 
 template <typename T, int D, bool kPaged>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(320, 1)
     prefix_tc5_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v_last,
                       const __grid_constant__ CUtensorMap tm_q)
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(352, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBarOff);
     uint64_t *empty = full + S::kSlots;
     uint64_t *q_full = empty + S::kSlots, *q_empty = q_full + 1;
-    uint64_t *s_full = q_full + 2, *p_half = s_full + 2, *p_full = p_half + 2, *pv_done = p_full + 2, *mma_done = pv_done + 2;
+    uint64_t *s_full = q_full + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *mma_done = pv_done + 2;
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + S::kMiscOff);
     volatile uint32_t *abort = misc + 1;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -131,16 +133,15 @@ __global__ void __launch_bounds__(352, 1)
     if (tid == 0) {
         for (int s = 0; s < S::kSlots; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);  // (both issuers)
+            mbar_init(&empty[s], 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 2);
+        mbar_init(q_empty, 1);
+        mbar_init(mma_done, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_half[i], 128);
             mbar_init(&p_full[i], 128);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&mma_done[i], 1);
         }
         misc[1] = 0u;
         fence_mbar_init();
@@ -246,36 +247,32 @@ __global__ void __launch_bounds__(352, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= 9) {
-        // ---- issuer of block x: one thread ----
-        const int x = warp - 9;
+    } else if (warp == 9) {
+        // ---- issuer: one thread ----
         if (elect_one()) {
             constexpr uint32_t kIdescS = tc5_idesc<kBf16>(128, S::kTK, false, false);
             constexpr uint32_t kIdescO = tc5_idesc<kBf16>(128, D, false, true);
             // (a descriptor's address field counts 16 bytes; slots and k-steps add to it)
-            const uint64_t desc_q = tc5_desc(smem_addr(smem + S::kQOff + x * S::kTileBytes), 0u, 1024u);
+            const uint64_t desc_q = tc5_desc(smem_addr(smem + S::kQOff), 0u, 1024u);
             const uint64_t desc_k = tc5_desc(smem_addr(smem), 0u, 1024u);
             const uint64_t desc_v = tc5_desc(smem_addr(smem), (uint32_t)S::kBoxBytes, 1024u);
-            const uint32_t t_s = tmem + S::kTmemS + x * 128, t_o = tmem + S::kTmemO + x * D;
             bool ok = true;
-            auto issue_s = [&](int slot) {
-                const uint64_t kd = desc_k + slot * (S::kTileBytes / 16);
-#pragma unroll 1
-                for (int ks = 0; ks < D / 16; ++ks) {  // (rolled: the tensor core sets the pace, and code this
-                                                       // warp runs rarely should be short)
+            auto issue_s = [&](int x, int slot) {
+                const uint64_t q = desc_q + x * (S::kTileBytes / 16), kd = desc_k + slot * (S::kTileBytes / 16);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
                     const int step = ((ks >> 2) * S::kBoxBytes + (ks & 3) * 32) / 16;
-                    tc5_mma_f16(t_s, desc_q + step, kd + step, kIdescS, ks > 0 ? 1u : 0u);
+                    tc5_mma_f16(tmem + S::kTmemS + x * 128, q + step, kd + step, kIdescS, ks > 0 ? 1u : 0u);
                 }
                 tc5_commit(&s_full[x]);
-                tc5_commit(&empty[slot]);
             };
-            auto issue_pv = [&](int slot, int half, bool first) {
+            auto issue_pv = [&](int x, int slot, bool first) {
                 const uint64_t vd = desc_v + slot * (S::kTileBytes / 16);
-#pragma unroll 1
-                for (int i = 0; i < S::kTK / 32; ++i) {
-                    const int ks = half * (S::kTK / 32) + i;
-                    tc5_mma_f16_ts(t_o, t_s + ks * 8, vd + ks * (16 * 128 / 16), kIdescO, (ks > 0 || !first) ? 1u : 0u);
-                }
+#pragma unroll
+                for (int ks = 0; ks < S::kTK / 16; ++ks)
+                    tc5_mma_f16_ts(tmem + S::kTmemO + x * D, tmem + S::kTmemS + x * 128 + ks * 8, vd + ks * (16 * 128 / 16),
+                                   kIdescO, (ks > 0 || !first) ? 1u : 0u);
+                tc5_commit(&pv_done[x]);
             };
             // the ring's next fill (K and V of each tile in turn), as slot and parity
             int slot = 0;
@@ -287,54 +284,57 @@ __global__ void __launch_bounds__(352, 1)
                 }
             };
             int u = u_lo, k = k_lo;
-            uint32_t pieces = 0u, n = 0u;  // pieces, and tiles of this block, so far
-            bool have_s = false;           // S of tile t is issued already
+            uint32_t pieces = 0u, n0 = 0u, n1 = 0u;  // pieces, and tiles of each block, so far
+            bool have_s = false;                     // S of tile t is issued already
             for (int t = lo; t < hi; ++t) {
-                const bool mine = (u % a.units_per_head) * a.unit_blocks + x < a.blocks && x < a.unit_blocks;
+                const bool two = a.unit_blocks > 1 && (u % a.units_per_head) * 2 + 1 < a.blocks;
                 const bool first = t == lo || k == 0;
                 const bool last = t == hi - 1 || k == a.n_tiles - 1;
-                if (first) {
-                    ok = prefix_wait(q_full, pieces & 1u, abort);
+                if (!have_s) {
+                    ok = prefix_wait(q_full, pieces & 1u, abort) && prefix_wait(&full[slot], par, abort);
                     ++pieces;
+                    // (S_X lies over the previous piece's last P_X)
+                    if (ok && n0 > 0u) ok = prefix_wait(&pv_done[0], (n0 - 1u) & 1u, abort);
+                    if (ok && two && n1 > 0u) ok = prefix_wait(&pv_done[1], (n1 - 1u) & 1u, abort);
                     if (!ok) break;
-                }
-                if (!mine) {  // (a unit of one block: the slots pass by)
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        ok = prefix_wait(&full[slot], par, abort);
-                        if (ok) mbar_arrive(&empty[slot]);
-                        step();
-                    }
-                    if (!ok) break;
-                    if (last) mbar_arrive(q_empty);
-                } else {
-                    if (!have_s) {
-                        // (S_X lies over the previous piece's last P_X)
-                        ok = prefix_wait(&full[slot], par, abort) && (n == 0u || prefix_wait(&pv_done[x], (n - 1u) & 1u, abort));
-                        if (!ok) break;
-                        tc5_fence_after();
-                        issue_s(slot);
-                        if (last) tc5_commit(q_empty);
-                        step();
-                    }
-                    const int vs = slot;
-                    if (!(ok = prefix_wait(&full[vs], par, abort) && prefix_wait(&p_half[x], n & 1u, abort))) break;
+                    tc5_fence_after();
+                    issue_s(0, slot);
+                    if (two) issue_s(1, slot);
+                    tc5_commit(&empty[slot]);
+                    if (last) tc5_commit(q_empty);
                     step();
-                    tc5_fence_after();
-                    issue_pv(vs, 0, first);
-                    if (!(ok = prefix_wait(&p_full[x], n & 1u, abort))) break;
-                    tc5_fence_after();
-                    issue_pv(vs, 1, first);
-                    tc5_commit(&pv_done[x]);
-                    tc5_commit(&empty[vs]);
-                    if (!last) {  // the next tile's S once this P . V is complete
-                        if (!(ok = prefix_wait(&full[slot], par, abort) && prefix_wait(&pv_done[x], n & 1u, abort))) break;
-                        issue_s(slot);
-                        if (t + 1 == hi - 1 || k + 1 == a.n_tiles - 1) tc5_commit(q_empty);
-                        step();
-                    }
-                    have_s = !last;
-                    ++n;
                 }
+                const int vs = slot;
+                if (!(ok = prefix_wait(&full[vs], par, abort) && prefix_wait(&p_full[0], n0 & 1u, abort))) break;
+                step();
+                const int ks = slot;  // the next tile's K
+                const bool next_last = t + 1 == hi - 1 || k + 1 == a.n_tiles - 1;
+                tc5_fence_after();
+                issue_pv(0, vs, first);
+                if (!two) tc5_commit(&empty[vs]);
+                if (!last) {  // the next tile's S of this block, once its P . V is complete
+                    if (!(ok = prefix_wait(&full[ks], par, abort) && prefix_wait(&pv_done[0], n0 & 1u, abort))) break;
+                    issue_s(0, ks);
+                    if (!two) tc5_commit(&empty[ks]);
+                }
+                ++n0;
+                if (two) {
+                    if (!(ok = prefix_wait(&p_full[1], n1 & 1u, abort))) break;
+                    tc5_fence_after();
+                    issue_pv(1, vs, first);
+                    tc5_commit(&empty[vs]);
+                    if (!last) {
+                        if (!(ok = prefix_wait(&pv_done[1], n1 & 1u, abort))) break;
+                        issue_s(1, ks);
+                        tc5_commit(&empty[ks]);
+                    }
+                    ++n1;
+                }
+                if (!last) {
+                    if (next_last) tc5_commit(q_empty);
+                    step();
+                }
+                have_s = !last;
                 if (++k == a.n_tiles) {
                     k = 0;
                     ++u;
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(352, 1)
                 *abort = 1u;
                 raise_error(a.err_word, KVD_DEVERR_TIMEOUT);
             }
-            tc5_commit(&mma_done[x]);  // this thread's products complete before the tensor memory is freed
-            mbar_wait_drain(&mma_done[x], 0u);
+            tc5_commit(mma_done);  // this thread's products complete before the tensor memory is freed
+            mbar_wait_drain(mma_done, 0u);
         }
         __syncwarp();
     } else {
@@ -427,8 +427,6 @@ __global__ void __launch_bounds__(352, 1)
                 };
                 weights(s0);
                 tc5_st32(t_s, pk);
-                tc5_fence_before();
-                mbar_arrive(&p_half[x]);
                 weights(s1);
                 tc5_st32(t_s + 32, pk);
                 float le, lo2;

@@ -6,7 +6,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "kvd_attention.cuh"
+#include "kvd_attention_stream.cuh"
 #include "kvd_host.cuh"
 
 namespace kvd {
@@ -378,6 +378,8 @@ struct Plan {
     bool tc5;         // tcgen05 kernel (128-row blocks, tiles and q by tensor map)
     bool early;       // small layer: kArgEarly, fewer CTAs per SM
     int cluster;      // > 0: cluster mode with this many CTAs per sequence-head
+    const void *stream_fn;  // modified scores, few rows: the streaming kernel (else null) ...
+    int max_splits, cta_tiles;  // ... its CTAs per head and the tiles of each
     size_t part_off, tickets_off, seg_off, state_off, ws_bytes;
 };
 
@@ -438,16 +440,72 @@ bool pick_scored_builds(kvd_dtype dtype, int D, int rb, bool paged, AttnVariant 
     }
 }
 
+// Modified scores, workspaces: at least this much room for the tickets.
+constexpr size_t kScoredTicketBytes = 256 * 1024;
+// The streaming kernel's CTAs: about this many for each one that is resident at
+// a time (1, 2 and 4: the long-context step 96.6 / 95.3 / 98.9 us, 16 x 12 heads
+// of 16 rows over documents 32.1 / 28.2 / 32.4), and at most this many slots
+// (CTAs that the longest heads would need).
+constexpr int kStreamRounds = 2;
+constexpr long long kStreamMaxSlots = 8192;
+// Modified scores over 16-bit caches with at most 16 query rows per KV head go
+// to the streaming kernel: the long-context step, capped, paged, 95.3 us against
+// 98.8 in the mma.sync kernel; a 1024-key window 32.4 / 34.6; documents with 16
+// rows 28.2 / 41.0; 128 sequences of 16 to 512 keys 28.5 / 47.4.
+bool use_stream(kvd_dtype dtype, int rows) { return (dtype == KVD_BF16 || dtype == KVD_F16) && rows <= 16; }
+
+// The plan of the streaming kernel (pl->rows is set).
+kvd_status make_stream_plan(int B, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype, Plan *pl, bool paged,
+                            long long keys, int window)
+{
+    int sms = 0;
+    const kvd_status st = current_sm_count(&sms);
+    if (st != KVD_OK) return st;
+    const long long heads = (long long)B * H_kv;
+    if (heads > 0x7fffffff) return KVD_ERR_UNSUPPORTED;
+    // Tiles per CTA: kStreamRounds rounds of CTAs over what the rows are
+    // expected to see (with a window: the window, a prefix beside it being
+    // short), whole rounds of the four warps, and not more slots than
+    // kStreamMaxSlots for what they may see at most.
+    const long long tiles = ((keys > 0 ? keys : (long long)max_past_len + N) + 63) / 64;
+    const long long expect = std::min<long long>(tiles, window > 0 ? ((long long)window + N) / 64 + 3 : tiles);
+    long long per = heads * expect / ((long long)kStreamRounds * stream_ctas_per_sm(D, pl->rows) * sms);
+    per = std::max(per, (heads * tiles + kStreamMaxSlots - 1) / kStreamMaxSlots);
+    per = std::min<long long>(std::max<long long>((per + 3) / 4 * 4, 4), std::max<long long>(tiles, 4));
+    pl->sms = sms;
+    pl->cta_tiles = (int)per;
+    pl->max_splits = (int)std::max<long long>((tiles + per - 1) / per, 1);
+    pl->stream_fn = dtype == KVD_BF16 ? stream_kernel_bf16(D, pl->rows, paged) : stream_kernel_f16(D, pl->rows, paged);
+    pl->early = pl->merge_pass = false;
+    pl->cluster = 0;
+    pl->launches = 1;
+    pl->rb = pl->rows;
+    pl->n_rowblocks = 1;
+    pl->tickets_off = 0;
+    size_t off = round_up(std::max((size_t)heads * sizeof(int), kScoredTicketBytes), 256);
+    pl->part_off = off;
+    // (any window's slots fit: no more than one per four tiles, nor than the bound)
+    const long long all_tiles = ((long long)max_past_len + N + 63) / 64;
+    const long long slots = std::max(std::min(heads * ((all_tiles + 3) / 4), kStreamMaxSlots + heads), heads * pl->max_splits);
+    off += round_up((size_t)slots * pl->rows * (D + 4) * sizeof(float), 256);
+    pl->seg_off = pl->state_off = off;
+    pl->ws_bytes = off;
+    return KVD_OK;
+}
+
 // scored: the kernels with modified scores.  keys: an upper bound on the keys
 // a sequence's rows see together (0: max_past_len + N).  states: the kernels
 // with modified scores leaving row states (no merge pass of their own, every
 // split described in the workspace).
 kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype,
-                     Plan *pl, bool paged = false, bool scored = false, long long keys = 0, bool states = false)
+                     Plan *pl, bool paged = false, bool scored = false, long long keys = 0, bool states = false,
+                     int window = 0)
 {
     kvd_status st = check_shapes(B, H_q, H_kv, D, N, max_past_len, dtype);
     if (st != KVD_OK) return st;
     pl->rows = (H_q / H_kv) * N;
+    pl->stream_fn = nullptr;
+    pl->max_splits = pl->cta_tiles = 0;
     // Many query rows per KV head (chunked decode with GQA): the tensor cores,
     // in blocks of 16 rows (mma.sync; E4M3 heads of at most 8 rows in the
     // swapped 8-row form) or, for 16-bit caches from kTc5MinRows rows, of 128
@@ -460,7 +518,9 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     pl->rb = pl->tc5 ? 128 : pl->mma ? 16 : pl->rows <= 1 ? 1 : pl->rows <= 2 ? 2 : (pl->rows <= 4 || dtype == KVD_E4M3) ? 4 : 8;
     pl->n_rowblocks = (pl->rows + pl->rb - 1) / pl->rb;
     AttnVariant vp, vt, op, ot;  // this layout's builds, and the other layout's
-    if (scored) {
+    if (scored && use_stream(dtype, pl->rows)) {
+        return make_stream_plan(B, H_kv, D, N, max_past_len, dtype, pl, paged, keys, window);
+    } else if (scored) {
         if (!pick_scored_builds(dtype, D, pl->rb, paged, &vp, &vt) || !pick_scored_builds(dtype, D, pl->rb, !paged, &op, &ot))
             return KVD_ERR_UNSUPPORTED;
     } else if (pl->tc5) {
@@ -554,13 +614,19 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     // (partial slots of blocks of 16 or more rows -- the tensor-core kernels'
     // but the 8-row E4M3 form -- hold only a block's real rows: the kernels'
     // part_rows<RB>)
+    // With modified scores the tickets come first, in a region that small shapes
+    // share: a workspace may then serve calls of different shapes in turn.
+    size_t off = 0;
+    pl->tickets_off = off;
+    if (scored) off += round_up(std::max((size_t)B * H_kv * pl->n_rowblocks * sizeof(int), kScoredTicketBytes), 256);
     const int part_rows = pl->rb >= 16 && pl->rows < pl->rb ? pl->rows : pl->rb;
     const size_t pieces = (size_t)sms * (occ > occ_other ? occ : occ_other) * 2 * part_rows;
-    size_t off = 0;
     pl->part_off = off;  // per piece row: o[D], m, l, 2 floats of padding (16-byte rows)
     off += round_up(pieces * (D + 4) * sizeof(float), 256);
-    pl->tickets_off = off;
-    off += round_up((size_t)B * H_kv * pl->n_rowblocks * sizeof(int), 256);
+    if (!scored) {
+        pl->tickets_off = off;
+        off += round_up((size_t)B * H_kv * pl->n_rowblocks * sizeof(int), 256);
+    }
     pl->seg_off = off;
     off += round_up((size_t)B * H_kv * pl->n_rowblocks * sizeof(int2), 256);
     pl->state_off = off;  // per query row: o[D], m, l, 2 floats of padding
@@ -763,12 +829,13 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
 
     Plan pl;
     if ((st = make_plan(B, H_q, H_kv, D, N, max_past_len, dtype, &pl, paged != nullptr, score != nullptr, keys,
-                        states)) != KVD_OK)
+                        states, score != nullptr ? score->window : 0)) != KVD_OK)
         return st;
     if (workspace == nullptr || workspace_bytes < pl.ws_bytes ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return KVD_ERR_WORKSPACE;
 
+    if (pl.stream_fn != nullptr && (st = kernel_ready(pl.stream_fn, 128, stream_smem_bytes(D, pl.rows))) != KVD_OK) return st;
     char *ws = static_cast<char *>(workspace);
     AttnScoredArgs a;  // (the kernels without modified scores take its AttnArgs part)
     a.q = q;
@@ -817,6 +884,7 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
         a.window = score->window;
         a.row_state = states ? reinterpret_cast<float *>(ws + pl.state_off) : nullptr;
     }
+    if (pl.stream_fn != nullptr) a.merge_state = ws + pl.tickets_off;
 
     // Both kernels are programmatic dependents of whatever precedes them on
     // the stream: they start early and wait (griddepcontrol.wait) before
@@ -829,6 +897,14 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void *args[] = {&a};
+    if (pl.stream_fn != nullptr) {
+        StreamArgs sa{pl.max_splits, pl.cta_tiles, states ? 1 : 0};
+        void *sargs[] = {&a, &sa};
+        cfg.gridDim = dim3((unsigned)(B * H_kv), (unsigned)pl.max_splits);
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = (size_t)stream_smem_bytes(D, pl.rows);
+        return cudaLaunchKernelExC(&cfg, pl.stream_fn, sargs) == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
+    }
     if (pl.cluster > 0) {  // one cluster of pl.cluster CTAs per sequence-head
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim.x = (unsigned)pl.cluster;
@@ -898,6 +974,8 @@ kvd_status row_state_plan(int B, int H_q, int H_kv, int D, int N, int max_past_l
     plan->rb = pl.rb;
     plan->n_rowblocks = pl.n_rowblocks;
     plan->prow = pl.rb >= 16 && pl.rows < pl.rb ? pl.rows : pl.rb;  // (the kernels' part_rows)
+    plan->max_splits = pl.stream_fn != nullptr ? pl.max_splits : 0;
+    plan->cta_tiles = pl.cta_tiles;
     plan->part_off = pl.part_off;
     plan->seg_off = pl.seg_off;
     plan->state_off = pl.state_off;

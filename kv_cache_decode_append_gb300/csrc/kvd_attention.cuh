@@ -1706,7 +1706,7 @@ template <typename T, int D, int RB, bool kTicketMerge, bool kPaged, typename C 
     return v;
 }
 
-// The same kernels with modified scores (kMod), attention only.
+// The same kernels with modified scores (kMod), attention only (fp32 caches).
 template <typename T, int D, int RB, bool kTicketMerge, bool kPaged> AttnVariant make_scored_variant()
 {
     using S = AttnShape<T, D, RB>;
@@ -1734,13 +1734,7 @@ template <typename T, int D, bool kTicketMerge, bool kPaged> bool pick_scored_rb
     case 1: *v = make_scored_variant<T, D, 1, kTicketMerge, kPaged>(); return true;
     case 2: *v = make_scored_variant<T, D, 2, kTicketMerge, kPaged>(); return true;
     case 4: *v = make_scored_variant<T, D, 4, kTicketMerge, kPaged>(); return true;
-    case 8:  // (16-bit rows of D = 128 take the tensor cores from 4 rows on)
-        if constexpr (sizeof(T) == 4 || D == 64) {
-            *v = make_scored_variant<T, D, 8, kTicketMerge, kPaged>();
-            return true;
-        } else {
-            return false;
-        }
+    case 8: *v = make_scored_variant<T, D, 8, kTicketMerge, kPaged>(); return true;
     default: return false;
     }
 }
@@ -1809,8 +1803,8 @@ bool attn_variant_tc5_bf16(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_bf16_tk(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_f16(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_f16_tk(int D, bool paged, AttnVariant *v);
-// modified scores: kvd_scored_{f32,bf16,f16}[_tk].cu (RB 1 .. 8: CUDA cores,
-// 16: mma.sync, 128: tcgen05)
+// modified scores: kvd_scored_{f32,bf16,f16}[_tk].cu (fp32: CUDA cores, RB 1 .. 8;
+// 16-bit: tcgen05, RB 128; 16-bit with fewer rows: kvd_attention_stream.cuh)
 bool attn_variant_scored_f32(int D, int RB, bool paged, AttnVariant *v);
 bool attn_variant_scored_f32_tk(int D, int RB, bool paged, AttnVariant *v);
 bool attn_variant_scored_bf16(int D, int RB, bool paged, AttnVariant *v);

@@ -117,13 +117,12 @@ template <typename S> __device__ __forceinline__ uint32_t mma_chunk_addr(uint32_
 //          for rows g and g+8
 // kMasked: per-key limits apply (lim: first key each row may not see), and
 // value rows at or past k_end are zeroed first.
-// kMod: the scores are modified and the rows' own bounds apply (mod), not lim.
-template <typename T, int D, bool kMasked, bool kMod = false>
+template <typename T, int D, bool kMasked>
 __device__ __forceinline__ void mma_tile(unsigned char *Ks, unsigned char *Vs,
                                          const uint32_t (&qa)[MmaShape<T, D>::kKSteps][4],
                                          float (&oacc)[MmaShape<T, D>::kNTiles][4], float (&m)[2],
                                          float (&l)[2], int warp, int lane, int tile_k0,
-                                         const int (&lim)[2], int k_end, float qscale, ModTile mod = ModTile{})
+                                         const int (&lim)[2], int k_end, float qscale)
 {
     using S = MmaShape<T, D>;
     const float kNegInf = __int_as_float(0xff800000);
@@ -168,32 +167,10 @@ __device__ __forceinline__ void mma_tile(unsigned char *Ks, unsigned char *Vs,
     }
 
     // ---- scale, mask, online softmax (rows g: e = 0,1; g+8: e = 2,3) ----
-    if constexpr (kMod) {
-        if (mod.sa->cap > 0.f) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sacc[nt][e] = cap_score<false>(sacc[nt][e] * qscale, mod.sa->cap, mod.sa->cap_in);
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sacc[nt][e] *= qscale;
-        }
-    }
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if constexpr (kMod) {
-                const int key = tile_k0 + kb + nt * 8 + 2 * t + (e & 1);
-                const RowScore &r = mod.rs[e >> 1];
-                sacc[nt][e] = fmaf(-r.slope, fabsf((float)(r.p - key)), sacc[nt][e]);
-                if constexpr (kMasked)
-                    if (key >= k_end || !row_sees(r, mod.pre, key)) sacc[nt][e] = kNegInf;
-                continue;
-            }
             sacc[nt][e] *= qscale;
             if constexpr (kMasked) {
                 const int key = tile_k0 + kb + nt * 8 + 2 * t + (e & 1);
@@ -231,19 +208,10 @@ __device__ __forceinline__ void mma_tile(unsigned char *Ks, unsigned char *Vs,
 
     // ---- value rows past the end of the sequence: zero (a NaN times 0 is NaN) ----
     if constexpr (kMasked) {
-        // (kMod: also keys that no row of the sequence sees, one lane a key)
-        uint32_t unseen = 0u;
-        bool stale = tile_k0 + kb + S::kKpw > k_end;
-        if constexpr (kMod) {
-            if (some_unseen(mod, tile_k0 + kb, S::kKpw, k_end))
-                unseen = __ballot_sync(0xffffffffu, lane < S::kKpw && key_unseen(mod, tile_k0 + kb + lane, k_end));
-            stale = unseen != 0u;
-        }
-        if (stale) {
+        if (tile_k0 + kb + S::kKpw > k_end) {
             for (int idx = lane; idx < S::kKpw * (D / 8); idx += 32) {
                 const int r = kb + idx / (D / 8), c = idx % (D / 8);
-                if (kMod ? (unseen >> (r - kb)) & 1u : tile_k0 + r >= k_end)
-                    sts128(mma_chunk_addr<S>(v_base, r, c), make_uint4(0u, 0u, 0u, 0u));
+                if (tile_k0 + r >= k_end) sts128(mma_chunk_addr<S>(v_base, r, c), make_uint4(0u, 0u, 0u, 0u));
             }
             fence_proxy_async_shared();  // before the slot is refilled by a bulk copy
             __syncwarp();
@@ -569,12 +537,9 @@ __device__ __forceinline__ void mma_insert_new_rows(unsigned char *Ks, unsigned 
 // viewed as [num_pages*H_kv*page_size, D] when kPaged).
 // C: the cache element type (T, or E4M3 codes with bf16 T: contiguous only).
 // kRows: rows per block, 16, or 8 for the swapped E4M3 form (mma_tile_e4m3_t).
-// kMod: modified scores and per-row bounds (AttnScoredArgs), attention only,
-// 16-bit caches.
-template <typename T, int D, bool kFused, bool kTicketMerge, bool kPaged, typename C = T, int kRows = 16,
-          bool kMod = false>
+template <typename T, int D, bool kFused, bool kTicketMerge, bool kPaged, typename C = T, int kRows = 16>
 __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T, D, C, kRows>::kMinBlocks)
-    attn_mma_kernel(const AttnArgsOf<kMod> a, const __grid_constant__ CUtensorMap tm_k,
+    attn_mma_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v)
 {
     using S = MmaShape<T, D, C, kRows>;
@@ -582,7 +547,6 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
     constexpr bool k8 = S::k8;
     constexpr bool kT8 = S::kT8;
     static_assert(!(k8 && kPaged), "the E4M3 cache is contiguous only");
-    static_assert(!kMod || (!kFused && !k8), "modified scores: attention over 16-bit caches");
     constexpr int RB = S::kRB;
     const float kNegInf = __int_as_float(0xff800000);
     extern __shared__ __align__(1024) unsigned char smem_mma[];
@@ -619,8 +583,7 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
 
-    RangeWalk<S, !kTicketMerge, kPaged, kMod> walk;
-    if constexpr (kMod) walk.window = a.window;
+    RangeWalk<S, !kTicketMerge, kPaged> walk;
     int issued = 0;
     if (warp == 0) {
         int carry = 0;
@@ -632,16 +595,7 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
                 const int P = __ldg(a.past_len + b);
                 const bool ok = past_len_ok(P, a.N, a.T_max, a.max_past_len);
                 if (!ok && blockIdx.x == 0) raise_error(a.err_word, KVD_DEVERR_PAST_LEN);
-                if constexpr (kMod) {
-                    if (ok) {
-                        const int2 db = seq_bounds(a, b, P);
-                        units = tile_regions<S::kTK>(P, a.N, a.window, db.x, db.y).n_tiles + S::kPieceUnits;
-                        pl[a.B + b] = db.x;
-                        pl[2 * a.B + b] = db.y;
-                    }
-                } else {
-                    units = ok ? (P + a.N + S::kTK - 1) / S::kTK + S::kPieceUnits : 0;
-                }
+                units = ok ? (P + a.N + S::kTK - 1) / S::kTK + S::kPieceUnits : 0;
                 pl[b] = P;
             }
             int v = units;
@@ -674,8 +628,6 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
     float m_run[2], l_run[2];
     float sfac[2];  // E4M3: per-row score factor (see mma_tile_e4m3)
     int lim[2];
-    RowScore rs[kMod ? 2 : 1];  // kMod: the bounds and penalties of rows g, g+8 ...
-    ModTile mod{};              // ... and the sequence's
     bool gave_up = false;  // this warp no longer waits for data (AbortCtl)
     int first_unwaited = -1;
     int n_pieces = 0;
@@ -721,12 +673,10 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
             // Q fragments of the 16 rows (rows past the block's rows are zero)
             const unsigned char *qs = smem + S::kQOff + s * S::kQSlotBytes;
             const int q_rows = min(RB, a.rows - mt.rb * RB);
-            if constexpr (kMod) mod = mod_tile(a, rs, mt.bh / a.H_kv, mt.P);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int rg = mt.rb * RB + (kT8 ? 2 * t + r : g + 8 * r);
                 lim[r] = mt.P + 1 + (rg % a.N);
-                if constexpr (kMod) rs[r] = row_score(a, mt.bh / a.H_kv, mt.bh % a.H_kv, rg, mt.P);
                 m_run[r] = kNegInf;
                 l_run[r] = 0.f;
             }
@@ -821,12 +771,6 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
 
         const int k_end = mt.tile_k0 + mt.nk;
         if (gave_up) {  // (computes nothing, writes nothing)
-        } else if constexpr (kMod) {
-            const bool all = row_sees_all<S::kTK>(rs[0], mod.pre, mt.tile_k0) && row_sees_all<S::kTK>(rs[1], mod.pre, mt.tile_k0);
-            if (__all_sync(0xffffffffu, all) && mt.nk == S::kTK)
-                mma_tile<T, D, false, true>(Ks, Vs, qa, oacc, m_run, l_run, warp, lane, mt.tile_k0, lim, k_end, a.qscale, mod);
-            else
-                mma_tile<T, D, true, true>(Ks, Vs, qa, oacc, m_run, l_run, warp, lane, mt.tile_k0, lim, k_end, a.qscale, mod);
         } else if (mt.tile_k0 + S::kTK <= mt.P + (kFused ? 0 : 1)) {
             if constexpr (kT8)
                 mma_tile_e4m3_t<D, false>(Ks, Vs, qa, oacc, m_run, l_run, warp, lane, mt.tile_k0, lim, k_end, sfac);
@@ -1001,22 +945,11 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
                 num = fmaf(wt, ep_o[(w * RB + r) * D + d], num);
                 den = fmaf(wt, ep_l[w * RB + r], den);
             }
-            if constexpr (kMod) {
-                if (single && a.row_state != nullptr) {
-                    float *pr = a.row_state + ((size_t)mt.bh * a.rows + rg) * (D + 4);
-                    pr[d] = num;
-                    if (d == 0) {
-                        pr[D] = M;
-                        pr[D + 1] = den;
-                    }
-                    continue;
-                }
-            }
             if (single) {
                 if constexpr (k8)  // values are stored / v_scale
                     Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d, num / den * a.kv_scale.y);
                 else
-                    Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d, quotient<kMod>(num, den));
+                    Tq::store(static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D + d, num / den);
             } else {
                 float *pr = a.part + (pbase + r) * (D + 4);
                 pr[d] = num;
@@ -1064,7 +997,7 @@ __global__ void __launch_bounds__(MmaShape<T, D, C, kRows>::kThreads, MmaShape<T
         for (int i = 0; i < 2; ++i) {
             const MergeJob job = jobs[i];
             if (i < n_pieces && job.n_chunks)
-                merge_pieces<T, D, RB, S::kThreads, k8, kMod>(a, job, nullptr, tid);  // (16-row heads: no scratch)
+                merge_pieces<T, D, RB, S::kThreads, k8>(a, job, nullptr, tid);  // (16-row heads: no scratch)
         }
     }
 
@@ -1098,37 +1031,6 @@ AttnVariant make_mma_variant()
     v.piece_units = S::kPieceUnits;
     v.tma = true;
     return v;
-}
-
-// The 16-row kernel with modified scores, attention only.
-template <typename T, int D, bool kTicketMerge, bool kPaged> AttnVariant make_scored_mma_variant()
-{
-    using S = MmaShape<T, D>;
-    AttnVariant v;
-    v.fn = reinterpret_cast<const void *>(&attn_mma_kernel<T, D, false, kTicketMerge, kPaged, T, 16, true>);
-    v.fused_fn = nullptr;
-    if constexpr (kTicketMerge) v.merge_fn = nullptr;
-    else v.merge_fn = reinterpret_cast<const void *>(&attn_merge_kernel<T, D, S::kRB, false, true>);
-    v.threads = S::kThreads;
-    v.fixed_smem_bytes = S::kFixedBytes;
-    v.tile_keys = S::kTK;
-    v.rows_per_block = S::kRB;
-    v.piece_units = S::kPieceUnits;
-    v.tma = true;
-    return v;
-}
-
-template <typename T, bool kTicketMerge> bool pick_scored_mma_variant(int D, bool paged, AttnVariant *v)
-{
-    switch (D) {
-    case 64:
-        *v = paged ? make_scored_mma_variant<T, 64, kTicketMerge, true>() : make_scored_mma_variant<T, 64, kTicketMerge, false>();
-        return true;
-    case 128:
-        *v = paged ? make_scored_mma_variant<T, 128, kTicketMerge, true>() : make_scored_mma_variant<T, 128, kTicketMerge, false>();
-        return true;
-    default: return false;
-    }
 }
 
 // bf16 q / out over an E4M3 cache: D = 128, contiguous; heads of at most 8

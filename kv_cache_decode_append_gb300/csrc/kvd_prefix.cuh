@@ -24,7 +24,7 @@
 // (u, c) has slot u + c: no slot is shared and there are at most units + G - 1.
 #pragma once
 
-#include "kvd_attention.cuh"
+#include "kvd_attention_stream.cuh"
 
 namespace kvd {
 
@@ -87,6 +87,7 @@ struct RowStateArgs {
     const int2 *seg;      // (first CTA, CTAs) per (b, h, row block)
     const int32_t *past_len;
     int rb, n_rowblocks, prow, T_max, max_past_len, N, grid;  // grid: the prefix kernel's CTAs
+    int max_splits, cta_tiles;  // max_splits > 0: part holds the streaming kernel's slots [B * H_kv][max_splits][gN][D + 4]
 };
 
 // Join: out[b, h, y, :] of 32 rows of a block and 32 columns per CTA: a warp
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
     const int c0 = blockIdx.y * (kJoinThreads / 32) + warp;   // column group
     const int bh = p.x * a.H_kv + h;
     const int P = __ldg(s.past_len + p.x);
-    const int2 seg = __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
+    const int2 seg = s.max_splits > 0 ? make_int2(0, 0) : __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
     if (!past_len_ok(P, s.N, s.T_max, s.max_past_len)) return;  // reported by the first launch
 
     const long long n = (long long)a.n_units * a.n_tiles;
@@ -136,8 +137,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
         M = Mn;
     };
     // the row's own keys
-    for (int j = 0; j < seg.y; ++j) {
-        const float *pr = seg.y == 1 ? s.state + ((size_t)bh * a.gN + p.y) * (D + 4)
+    const int own = s.max_splits > 0 ? stream_splits((P + s.N + 63) / 64, s.cta_tiles, s.max_splits) : seg.y;
+    for (int j = 0; j < own; ++j) {
+        const float *pr = s.max_splits > 0 ? s.part + (((size_t)bh * s.max_splits + j) * a.gN + p.y) * (D + 4)
+                          : seg.y == 1 ? s.state + ((size_t)bh * a.gN + p.y) * (D + 4)
                                      : s.part + (((size_t)(seg.x + j) * 2 + (j == 0)) * s.prow + p.y % s.rb) * (D + 4);
         const float4 o = __ldcg(reinterpret_cast<const float4 *>(pr) + c0);
         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pr + D));

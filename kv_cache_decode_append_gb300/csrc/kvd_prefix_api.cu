@@ -167,6 +167,8 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     s.rb = pl.own.rb;
     s.n_rowblocks = pl.own.n_rowblocks;
     s.prow = pl.own.prow;
+    s.max_splits = pl.own.max_splits;
+    s.cta_tiles = pl.own.cta_tiles;
     s.T_max = T_max;
     s.max_past_len = max_past_len;
     s.N = N;

@@ -25,15 +25,6 @@ template <int D> struct PrefixSimtShape {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-// 16 bytes global -> shared, asynchronously; zeros when !real (src is not read).
-__device__ __forceinline__ void cp_async16(float *dst, const float *src, bool real)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(real ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait_all_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(256, 1) prefix_simt_kernel(const PrefixArgs a)
 {
@@ -69,7 +60,7 @@ __global__ void __launch_bounds__(256, 1) prefix_simt_kernel(const PrefixArgs a)
                     row = (size_t)h * a.S_max + key;
                 }
             }
-            cp_async16(dst + r * stride + c, base + row * D + c, real);
+            cp_async16(smem_addr(dst + r * stride + c), base + row * D + c, real);
         }
         cp_async_commit();
     };
@@ -105,7 +96,7 @@ __global__ void __launch_bounds__(256, 1) prefix_simt_kernel(const PrefixArgs a)
                     for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
             }
         }
-        cp_async_wait_all_but_one();  // K of this tile
+        cp_async_wait<1>();  // K of this tile
         __syncthreads();
         float s[8][4];
 #pragma unroll
@@ -157,7 +148,7 @@ __global__ void __launch_bounds__(256, 1) prefix_simt_kernel(const PrefixArgs a)
                 ps[(8 * ty + i) * S::kPStride + tx + 16 * j] = p;
             }
         }
-        cp_async_wait_all_but_one();  // V of this tile
+        cp_async_wait<1>();  // V of this tile
         __syncthreads();
 #pragma unroll 2
         for (int kk = 0; kk < S::kTK; kk += 4) {

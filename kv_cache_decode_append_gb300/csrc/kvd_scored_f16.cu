@@ -1,14 +1,10 @@
-// Instantiates the f16 attention kernels with modified scores, the separate merge pass:
-// CUDA cores (RB 1 .. 8), mma.sync (RB 16), tcgen05 (RB 128).
-#include "kvd_attention.cuh"
-#include "kvd_attention_mma.cuh"
+// Instantiates the f16 tcgen05 attention kernels with modified scores (RB 128),
+// the separate merge pass.
 #include "kvd_attention_tc5.cuh"
 
 namespace kvd {
 bool attn_variant_scored_f16(int D, int RB, bool paged, AttnVariant *v)
 {
-    if (RB == 128) return pick_scored_tc5_variant<__half, false>(D, paged, v);
-    if (RB == 16) return pick_scored_mma_variant<__half, false>(D, paged, v);
-    return pick_scored_variant<__half, false>(D, RB, paged, v);
+    return RB == 128 && pick_scored_tc5_variant<__half, false>(D, paged, v);
 }
 }  // namespace kvd

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "kvd_attention_stream.cuh"
+#include "kvd_prefix.cuh"
 #include "kvd_host.cuh"
 
 namespace kvd {
@@ -380,6 +381,8 @@ struct Plan {
     int cluster;      // > 0: cluster mode with this many CTAs per sequence-head
     const void *stream_fn;  // modified scores, few rows: the streaming kernel (else null) ...
     int max_splits, cta_tiles;  // ... its CTAs per head and the tiles of each
+    bool pair;              // modified scores, many rows: the pair kernel ...
+    PairVariant pv;
     size_t part_off, tickets_off, seg_off, state_off, ws_bytes;
 };
 
@@ -427,17 +430,6 @@ kvd_status min_occupancy(int dev, const AttnVariant &vp, const AttnVariant &vt, 
         if (o < *occ) *occ = o;
     }
     return KVD_OK;
-}
-
-// The two builds with modified scores, by row block (16: mma.sync, 128: tcgen05).
-bool pick_scored_builds(kvd_dtype dtype, int D, int rb, bool paged, AttnVariant *vp, AttnVariant *vt)
-{
-    switch (dtype) {
-    case KVD_F32: return attn_variant_scored_f32(D, rb, paged, vp) && attn_variant_scored_f32_tk(D, rb, paged, vt);
-    case KVD_BF16: return attn_variant_scored_bf16(D, rb, paged, vp) && attn_variant_scored_bf16_tk(D, rb, paged, vt);
-    case KVD_F16: return attn_variant_scored_f16(D, rb, paged, vp) && attn_variant_scored_f16_tk(D, rb, paged, vt);
-    default: return false;
-    }
 }
 
 // Modified scores, workspaces: at least this much room for the tickets.
@@ -493,6 +485,39 @@ kvd_status make_stream_plan(int B, int H_kv, int D, int N, int max_past_len, kvd
     return KVD_OK;
 }
 
+// The plan of the pair kernel (pl->rows is set).
+kvd_status make_pair_plan(int B, int H_q, int H_kv, int D, int N, kvd_dtype dtype, Plan *pl, bool paged, bool states)
+{
+    const bool ok = dtype == KVD_BF16 ? pair_variant_bf16(D, paged, &pl->pv) : pair_variant_f16(D, paged, &pl->pv);
+    if (!ok) return KVD_ERR_UNSUPPORTED;
+    int sms = 0;
+    const kvd_status st = current_sm_count(&sms);
+    if (st != KVD_OK) return st;
+    const size_t smem = (size_t)pl->pv.fixed_smem_bytes + round_up(((size_t)4 * B + 1) * sizeof(int), 16);
+    if (smem > (size_t)kMaxSmemPerCta) return KVD_ERR_UNSUPPORTED;
+    const int blocks = (pl->rows + 127) / 128;
+    const size_t slot_rows = pl->rows > 128 ? 256 : 128;
+    if ((long long)B * H_kv * blocks * 4 > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;
+    pl->pair = true;
+    pl->sms = pl->grid = sms;
+    pl->smem = (int)smem;
+    pl->rb = 256;
+    pl->n_rowblocks = (blocks + 1) / 2;
+    pl->early = pl->merge_pass = false;
+    pl->cluster = 0;
+    pl->launches = 2;
+    pl->tickets_off = 0;  // (none; the region is the other kernels', left alone)
+    size_t off = kScoredTicketBytes;
+    pl->part_off = off;  // two slots per CTA: o, then m and l
+    off += round_up((size_t)2 * sms * slot_rows * (D + 2) * sizeof(float), 256);
+    pl->seg_off = off;
+    off += round_up((size_t)B * H_kv * pl->n_rowblocks * sizeof(int2), 256);
+    pl->state_off = off;
+    if (states) off += round_up((size_t)B * H_q * N * (D + 4) * sizeof(float), 256);
+    pl->ws_bytes = off;
+    return KVD_OK;
+}
+
 // scored: the kernels with modified scores.  keys: an upper bound on the keys
 // a sequence's rows see together (0: max_past_len + N).  states: the kernels
 // with modified scores leaving row states (no merge pass of their own, every
@@ -505,6 +530,7 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     if (st != KVD_OK) return st;
     pl->rows = (H_q / H_kv) * N;
     pl->stream_fn = nullptr;
+    pl->pair = false;
     pl->max_splits = pl->cta_tiles = 0;
     // Many query rows per KV head (chunked decode with GQA): the tensor cores,
     // in blocks of 16 rows (mma.sync; E4M3 heads of at most 8 rows in the
@@ -520,8 +546,11 @@ kvd_status make_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, k
     AttnVariant vp, vt, op, ot;  // this layout's builds, and the other layout's
     if (scored && use_stream(dtype, pl->rows)) {
         return make_stream_plan(B, H_kv, D, N, max_past_len, dtype, pl, paged, keys, window);
+    } else if (scored && f16_family) {
+        return make_pair_plan(B, H_q, H_kv, D, N, dtype, pl, paged, states);
     } else if (scored) {
-        if (!pick_scored_builds(dtype, D, pl->rb, paged, &vp, &vt) || !pick_scored_builds(dtype, D, pl->rb, !paged, &op, &ot))
+        if (dtype != KVD_F32 || !attn_variant_scored_f32(D, pl->rb, paged, &vp) || !attn_variant_scored_f32_tk(D, pl->rb, paged, &vt) ||
+            !attn_variant_scored_f32(D, pl->rb, !paged, &op) || !attn_variant_scored_f32_tk(D, pl->rb, !paged, &ot))
             return KVD_ERR_UNSUPPORTED;
     } else if (pl->tc5) {
         const auto builds = [&](bool pg, AttnVariant *p, AttnVariant *t) {
@@ -836,6 +865,7 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
         return KVD_ERR_WORKSPACE;
 
     if (pl.stream_fn != nullptr && (st = kernel_ready(pl.stream_fn, 128, stream_smem_bytes(D, pl.rows))) != KVD_OK) return st;
+    if (pl.pair && (st = kernel_ready(pl.pv.fn, 320, pl.smem)) != KVD_OK) return st;
     char *ws = static_cast<char *>(workspace);
     AttnScoredArgs a;  // (the kernels without modified scores take its AttnArgs part)
     a.q = q;
@@ -885,6 +915,7 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
         a.row_state = states ? reinterpret_cast<float *>(ws + pl.state_off) : nullptr;
     }
     if (pl.stream_fn != nullptr) a.merge_state = ws + pl.tickets_off;
+    if (pl.pair) a.merge_state = ws + pl.seg_off;
 
     // Both kernels are programmatic dependents of whatever precedes them on
     // the stream: they start early and wait (griddepcontrol.wait) before
@@ -904,6 +935,32 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = (size_t)stream_smem_bytes(D, pl.rows);
         return cudaLaunchKernelExC(&cfg, pl.stream_fn, sargs) == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
+    }
+    if (pl.pair) {
+        // (column, row, head, page or sequence) of the caches, (column, row) of q
+        const uint64_t per = paged != nullptr ? (uint64_t)paged->page_size : (uint64_t)T_max;
+        const uint64_t row_b = (uint64_t)D * 2, strides[3] = {row_b, per * row_b, per * row_b * H_kv};
+        const uint64_t dims[4] = {(uint64_t)D, per, (uint64_t)H_kv, paged != nullptr ? (uint64_t)paged->num_pages : (uint64_t)B};
+        const uint32_t box[4] = {64, 64, 1, 1}, qbox[4] = {64, 128, 1, 1};
+        const uint64_t q_rows = (uint64_t)B * H_q * N, qdims[4] = {(uint64_t)D, q_rows, 1, 1};
+        const uint64_t qstrides[3] = {row_b, q_rows * row_b, q_rows * row_b};
+        if (q_rows + 256 > 0x7fffffffULL) return KVD_ERR_UNSUPPORTED;  // 32-bit box coordinates
+        alignas(64) CUtensorMap tmk, tmv, tmq;
+        if ((st = encode_map_16bit(&tmk, k_cache, dtype, 4, dims, strides, box)) != KVD_OK) return st;
+        if ((st = encode_map_16bit(&tmv, v_cache, dtype, 4, dims, strides, box)) != KVD_OK) return st;
+        if ((st = encode_map_16bit(&tmq, q, dtype, 4, qdims, qstrides, qbox)) != KVD_OK) return st;
+        void *pargs[] = {&a, &tmk, &tmv, &tmv, &tmq};
+        cfg.gridDim = dim3((unsigned)pl.grid);
+        cfg.blockDim = dim3(320);
+        cfg.dynamicSmemBytes = (size_t)pl.smem;
+        if (cudaLaunchKernelExC(&cfg, pl.pv.fn, pargs) != cudaSuccess) return KVD_ERR_CUDA;
+        if (states) return KVD_OK;
+        int grid = pl.grid, blocks = (pl.rows + 127) / 128;
+        void *jargs[] = {&a, &grid, &blocks};
+        cfg.gridDim = dim3((unsigned)(B * H_kv * blocks * 4), (unsigned)(D / 4 / (kJoinThreads / 32)));
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.dynamicSmemBytes = 0;
+        return cudaLaunchKernelExC(&cfg, pl.pv.join_fn, jargs) == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
     }
     if (pl.cluster > 0) {  // one cluster of pl.cluster CTAs per sequence-head
         attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -974,6 +1031,7 @@ kvd_status row_state_plan(int B, int H_q, int H_kv, int D, int N, int max_past_l
     plan->rb = pl.rb;
     plan->n_rowblocks = pl.n_rowblocks;
     plan->prow = pl.rb >= 16 && pl.rows < pl.rb ? pl.rows : pl.rb;  // (the kernels' part_rows)
+    plan->pair_grid = pl.pair ? pl.grid : 0;
     plan->max_splits = pl.stream_fn != nullptr ? pl.max_splits : 0;
     plan->cta_tiles = pl.cta_tiles;
     plan->part_off = pl.part_off;

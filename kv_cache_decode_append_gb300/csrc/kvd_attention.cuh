@@ -156,6 +156,18 @@ __device__ __forceinline__ bool row_sees(const RowScore &r, int pre, int key)
     return key >= r.doc && (key < pre || (key >= r.lo && key <= r.p));
 }
 
+// Two scores capped as below with one reciprocal: 1 / a and 1 / b from 1 / (a b)
+// (the exponents limited to 2^60: tanh is 1 in fp32 from 2^26 on).
+__device__ __forceinline__ void cap_score_pair(float &y0, float &y1, float C, float cap_in)
+{
+    const float e0 = 1.f + fast_exp2(fminf(y0 * cap_in, 60.f)), e1 = 1.f + fast_exp2(fminf(y1 * cap_in, 60.f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e0 * e1));
+    r *= -2.f * C;
+    y0 = fmaf(r, e1, C);
+    y1 = fmaf(r, e0, C);
+}
+
 // C tanh(y0 / C).  For 16-bit results tanh z = 1 - 2 / (1 + e^2z) with the
 // approximate exp2 and reciprocal: off by at most about 2^-21 absolutely, which
 // moves a weight by C 2^-21 relatively (cap 50: 3e-5, a hundredth of a bf16
@@ -1803,13 +1815,9 @@ bool attn_variant_tc5_bf16(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_bf16_tk(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_f16(int D, bool paged, AttnVariant *v);
 bool attn_variant_tc5_f16_tk(int D, bool paged, AttnVariant *v);
-// modified scores: kvd_scored_{f32,bf16,f16}[_tk].cu (fp32: CUDA cores, RB 1 .. 8;
-// 16-bit: tcgen05, RB 128; 16-bit with fewer rows: kvd_attention_stream.cuh)
+// modified scores, fp32: kvd_scored_f32[_tk].cu (16-bit caches: kvd_attention_stream.cuh
+// and kvd_pair_tc5.cuh)
 bool attn_variant_scored_f32(int D, int RB, bool paged, AttnVariant *v);
 bool attn_variant_scored_f32_tk(int D, int RB, bool paged, AttnVariant *v);
-bool attn_variant_scored_bf16(int D, int RB, bool paged, AttnVariant *v);
-bool attn_variant_scored_bf16_tk(int D, int RB, bool paged, AttnVariant *v);
-bool attn_variant_scored_f16(int D, int RB, bool paged, AttnVariant *v);
-bool attn_variant_scored_f16_tk(int D, int RB, bool paged, AttnVariant *v);
 
 }  // namespace kvd

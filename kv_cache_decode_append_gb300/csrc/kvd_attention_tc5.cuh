@@ -256,10 +256,9 @@ __device__ __forceinline__ void named_barrier_sync(int id, int threads)
 // the tile (and, by row block 0, into the cache: kc / vc address the cache row
 // of the tile's first key); value rows at or past the sequence end are zeroed
 // (a zero weight times a stale NaN is NaN inside the MMA).
-// kMod: value rows of keys that no row of the sequence sees (mod) likewise.
-template <typename T, int D, bool kFused, bool kMod = false>
+template <typename T, int D, bool kFused>
 __device__ __forceinline__ void tc5_fix_tile(const AttnArgs &a, uint32_t Ks, uint32_t Vs, const TileMeta &mt,
-                                             unsigned char *kc, unsigned char *vc, int lane, ModTile mod = ModTile{})
+                                             unsigned char *kc, unsigned char *vc, int lane)
 {
     using S = Tc5Shape<T, D>;
     constexpr int kChunks = S::kRowBytes / 16;
@@ -301,27 +300,16 @@ __device__ __forceinline__ void tc5_fix_tile(const AttnArgs &a, uint32_t Ks, uin
             }
         }
     }
-    if constexpr (kMod) {
-#pragma unroll
-        for (int half = 0; half < S::kTK; half += 32) {  // (one lane a key)
-            uint32_t unseen = __ballot_sync(0xffffffffu, key_unseen(mod, mt.tile_k0 + half + lane, k_end));
-            for (; unseen != 0u; unseen &= unseen - 1u) {
-                const int r = half + __ffs((int)unseen) - 1;
-                if (lane < kChunks) sts128(tc5_chunk_addr<S>(Vs, r, lane), make_uint4(0u, 0u, 0u, 0u));
-            }
-        }
-    } else {
-        for (int idx = lane; idx < (S::kTK - mt.nk) * kChunks; idx += 32) {
-            const int r = mt.nk + idx / kChunks, c = idx % kChunks;
-            sts128(tc5_chunk_addr<S>(Vs, r, c), make_uint4(0u, 0u, 0u, 0u));
-        }
+    for (int idx = lane; idx < (S::kTK - mt.nk) * kChunks; idx += 32) {
+        const int r = mt.nk + idx / kChunks, c = idx % kChunks;
+        sts128(tc5_chunk_addr<S>(Vs, r, c), make_uint4(0u, 0u, 0u, 0u));
     }
 }
 
 // Log-sum-exp merge of a split head's pieces, one warp per query row (the
 // four softmax warps share the rows): the pieces' partials were written by the
 // CTAs c_first .. c_first + n_chunks - 1 (slot 1 of the first, else slot 0).
-template <typename T, int D, bool kMod = false>
+template <typename T, int D>
 __device__ __forceinline__ void tc5_merge_rows(const AttnArgs &a, const MergeJob &job, int warp, int lane)
 {
     using Tq = Elem<T>;
@@ -350,21 +338,19 @@ __device__ __forceinline__ void tc5_merge_rows(const AttnArgs &a, const MergeJob
         }
         T *dst = static_cast<T *>(a.out) + ((size_t)job.bh * a.rows + job.rb * kRB + r) * D + lane * kDpl;
 #pragma unroll
-        for (int i = 0; i < kDpl; ++i) Tq::store(dst + i, quotient<kMod>(acc[i], den));
+        for (int i = 0; i < kDpl; ++i) Tq::store(dst + i, acc[i] / den);
     }
 }
 
 // The kernel.  kFused: append + attention (kvd_decode_step); kTicketMerge:
 // split heads merged at the end of the kernel by the CTA that completes them,
 // else by the separate merge pass; kPaged: tiles from a page pool.
-// kMod: modified scores and per-row bounds (AttnScoredArgs), attention only.
-template <typename T, int D, bool kFused, bool kTicketMerge, bool kPaged, bool kMod = false>
+template <typename T, int D, bool kFused, bool kTicketMerge, bool kPaged>
 __global__ void __launch_bounds__(224, 1)
-    attn_tc5_kernel(const AttnArgsOf<kMod> a, const __grid_constant__ CUtensorMap tm_k,
+    attn_tc5_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q)
 {
     using S = Tc5Shape<T, D>;
-    static_assert(!kMod || !kFused, "modified scores: attention only");
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kRescaleThreshold = 8.0f;
     const float kNegInf = __int_as_float(0xff800000);
@@ -435,16 +421,7 @@ __global__ void __launch_bounds__(224, 1)
                 const int P = __ldg(a.past_len + b);
                 const bool ok = past_len_ok(P, a.N, a.T_max, a.max_past_len);
                 if (!ok && blockIdx.x == 0) raise_error(a.err_word, KVD_DEVERR_PAST_LEN);
-                if constexpr (kMod) {
-                    if (ok) {
-                        const int2 db = seq_bounds(a, b, P);
-                        units = tile_regions<S::kTK>(P, a.N, a.window, db.x, db.y).n_tiles + S::kPieceUnits;
-                        pl[a.B + b] = db.x;
-                        pl[2 * a.B + b] = db.y;
-                    }
-                } else {
-                    units = ok ? (P + a.N + S::kTK - 1) / S::kTK + S::kPieceUnits : 0;
-                }
+                units = ok ? (P + a.N + S::kTK - 1) / S::kTK + S::kPieceUnits : 0;
                 pl[b] = P;
             }
             int v = units;
@@ -458,8 +435,7 @@ __global__ void __launch_bounds__(224, 1)
         }
         __syncwarp();
         if (lane == 0) {
-            RangeWalk<S, !kTicketMerge, kPaged, kMod> walk;
-            if constexpr (kMod) walk.window = a.window;
+            RangeWalk<S, !kTicketMerge, kPaged> walk;
             const int HR = a.H_kv * a.n_rowblocks;
             const long long n_total = (long long)pre[a.B] * HR;
             const long long G = min((long long)gridDim.x, n_total);
@@ -515,7 +491,6 @@ __global__ void __launch_bounds__(224, 1)
         constexpr uint32_t kIdescS = tc5_idesc<kBf16>(128, S::kTK, false, false);
         bool dead = false;
         int n_pieces = 0;
-        ModTile mod{};
         for (int pos = 0;; ++pos) {
             const int st = pos % S::kStages;
             int ok = 1;
@@ -530,14 +505,7 @@ __global__ void __launch_bounds__(224, 1)
             const bool first = (mt.flags & kMetaFirst) != 0;
             if (first) ++n_pieces;
             const uint32_t kt = ring + st * 2 * S::kTileBytes;
-            if constexpr (kMod) {
-                if (first) mod = mod_tile(a, nullptr, mt.bh / a.H_kv, mt.P);
-                if (some_unseen(mod, mt.tile_k0, S::kTK, mt.tile_k0 + mt.nk)) {
-                    tc5_fix_tile<T, D, false, true>(a, kt, kt + S::kTileBytes, mt, nullptr, nullptr, lane, mod);
-                    fence_proxy_async_shared();  // generic writes before the tensor core reads the tile
-                    __syncwarp();
-                }
-            } else if ((kFused && mt.tile_k0 + S::kTK > mt.P) || mt.nk < S::kTK) {
+            if ((kFused && mt.tile_k0 + S::kTK > mt.P) || mt.nk < S::kTK) {
                 unsigned char *kc = nullptr, *vc = nullptr;
                 if constexpr (kFused) {
                     size_t crow = 0;  // cache row of the tile's first key
@@ -634,8 +602,6 @@ __global__ void __launch_bounds__(224, 1)
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
         float m_run = kNegInf, l_run = 0.f;
         int lim = 0;
-        RowScore rs{};  // kMod: the row's bounds and penalty, and the prefix its sequence sees
-        int pre_len = 0;
         int pe_cnt[2] = {0, 0};   // completions of p_empty[b] waited for
         int n_split = 0;          // split pieces computed (ticket merge)
         bool dead = false;
@@ -664,10 +630,6 @@ __global__ void __launch_bounds__(224, 1)
             const bool first = (mt.flags & kMetaFirst) != 0;
             if (first) {
                 lim = mt.P + 1 + ((mt.rb * S::kRB + r) % a.N);
-                if constexpr (kMod) {
-                    rs = row_score(a, mt.bh / a.H_kv, mt.bh % a.H_kv, mt.rb * S::kRB + r, mt.P);
-                    pre_len = seq_bounds(a, mt.bh / a.H_kv, mt.P).y;
-                }
                 m_run = kNegInf;
                 l_run = 0.f;
             }
@@ -686,47 +648,19 @@ __global__ void __launch_bounds__(224, 1)
             // (their rows may hold stale NaN).  The row max is taken on the raw
             // scores (qscale > 0) and the scale folded into the exponent; max
             // and sum run as 8 independent chains (a row is one thread).
-            if constexpr (kMod) {
-                // the modified scores (log2 units) in place of the raw ones; bounds
-                // alone leave them raw, and the scale in the exponent as below
-                if (a.cap > 0.f) {
+            const bool masked = mt.tile_k0 + S::kTK > mt.P + 1;
+            if (masked) {
 #pragma unroll
-                    for (int c = 0; c < S::kTK; ++c)
-                        sr[c] = __float_as_uint(cap_score<false>(__uint_as_float(sr[c]) * a.qscale, a.cap, a.cap_in));
-                } else if (a.slopes != nullptr) {
-#pragma unroll
-                    for (int c = 0; c < S::kTK; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.qscale);
-                }
-                if (a.slopes != nullptr) {
-                    const float d0 = (float)(rs.p - mt.tile_k0);  // (whole numbers: d0 - c is exact below 2^24)
-#pragma unroll
-                    for (int c = 0; c < S::kTK; ++c)
-                        sr[c] = __float_as_uint(fmaf(-rs.slope, fabsf(d0 - (float)c), __uint_as_float(sr[c])));
-                }
-                if (mt.nk < S::kTK || !row_sees_all<S::kTK>(rs, pre_len, mt.tile_k0)) {
-                    const int k_end = mt.tile_k0 + mt.nk;
-#pragma unroll
-                    for (int c = 0; c < S::kTK; ++c)
-                        if (mt.tile_k0 + c >= k_end || !row_sees(rs, pre_len, mt.tile_k0 + c)) sr[c] = 0xff800000u;
-                }
-            } else {
-                const bool masked = mt.tile_k0 + S::kTK > mt.P + 1;
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < S::kTK; ++c)
-                        if (mt.tile_k0 + c >= lim) sr[c] = 0xff800000u;  // -inf
-                }
+                for (int c = 0; c < S::kTK; ++c)
+                    if (mt.tile_k0 + c >= lim) sr[c] = 0xff800000u;  // -inf
             }
-            float qscale = a.qscale;
-            if constexpr (kMod)
-                if (a.cap > 0.f || a.slopes != nullptr) qscale = 1.f;
             float mx8[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(sr[i]);
 #pragma unroll
             for (int c = 8; c < S::kTK; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], __uint_as_float(sr[c]));
             const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                   fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * qscale;
+                                   fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * a.qscale;
             float alpha = 1.f;
             bool rescale = false;
             if (mx > m_run + kRescaleThreshold) {
@@ -743,8 +677,8 @@ __global__ void __launch_bounds__(224, 1)
             uint32_t pk[S::kTK / 2];
 #pragma unroll
             for (int c = 0; c < S::kTK / 2; ++c) {
-                const float p0 = fast_exp2(fmaf(__uint_as_float(sr[2 * c]), qscale, nmu));
-                const float p1 = fast_exp2(fmaf(__uint_as_float(sr[2 * c + 1]), qscale, nmu));
+                const float p0 = fast_exp2(fmaf(__uint_as_float(sr[2 * c]), a.qscale, nmu));
+                const float p1 = fast_exp2(fmaf(__uint_as_float(sr[2 * c + 1]), a.qscale, nmu));
                 l8[c & 7] += p0 + p1;
                 pk[c] = pack_pair<T>(p0, p1);
             }
@@ -788,7 +722,7 @@ __global__ void __launch_bounds__(224, 1)
             const int rg = mt.rb * S::kRB + r;
             const bool real = rg < a.rows;  // (every lane loads: the loads are warp-collective)
             {
-                const float inv = kMod && l_run == 0.f ? 0.f : 1.f / l_run;  // (a row that sees nothing: zeros)
+                const float inv = 1.f / l_run;
                 float *pr = nullptr;
                 T *orow = static_cast<T *>(a.out) + ((size_t)mt.bh * a.rows + rg) * D;
                 if (!single) {
@@ -796,19 +730,12 @@ __global__ void __launch_bounds__(224, 1)
                         ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == mt.c_first ? 1 : 0)) * part_rows<S::kRB>(a.rows);
                     pr = a.part + (pbase + r) * (D + 4);
                 }
-                bool to_out = single;
-                if constexpr (kMod) {
-                    if (single && a.row_state != nullptr) {
-                        pr = a.row_state + ((size_t)mt.bh * a.rows + rg) * (D + 4);
-                        to_out = false;
-                    }
-                }
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
                     tc5_ld32(lane_addr + S::kTmemO + c0, o);
                     if (!real) continue;
-                    if (to_out) {
+                    if (single) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             stg128(orow + c0 + i,
@@ -822,7 +749,7 @@ __global__ void __launch_bounds__(224, 1)
                             *reinterpret_cast<uint4 *>(pr + c0 + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
-                if (real && !to_out) *reinterpret_cast<float2 *>(pr + D) = make_float2(m_run, l_run);
+                if (real && !single) *reinterpret_cast<float2 *>(pr + D) = make_float2(m_run, l_run);
             }
             tc5_fence_before();  // (the next arrive on p_full orders these reads before O is overwritten)
             if constexpr (kTicketMerge) {
@@ -861,7 +788,7 @@ __global__ void __launch_bounds__(224, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const MergeJob job = jobs[i];
-                if (i < n_split && job.n_chunks) tc5_merge_rows<T, D, kMod>(a, job, warp, lane);
+                if (i < n_split && job.n_chunks) tc5_merge_rows<T, D>(a, job, warp, lane);
             }
         }
     }
@@ -890,38 +817,6 @@ template <typename T, int D, bool kTicketMerge, bool kPaged> AttnVariant make_tc
     v.tma = true;
     v.q_map = true;
     return v;
-}
-
-// The kernel with modified scores, attention only.
-template <typename T, int D, bool kTicketMerge, bool kPaged> AttnVariant make_scored_tc5_variant()
-{
-    using S = Tc5Shape<T, D>;
-    AttnVariant v;
-    v.fn = reinterpret_cast<const void *>(&attn_tc5_kernel<T, D, false, kTicketMerge, kPaged, true>);
-    v.fused_fn = nullptr;
-    if constexpr (kTicketMerge) v.merge_fn = nullptr;
-    else v.merge_fn = reinterpret_cast<const void *>(&attn_merge_kernel<T, D, S::kRB, false, true>);
-    v.threads = S::kThreads;
-    v.fixed_smem_bytes = S::kFixedBytes;
-    v.tile_keys = S::kTK;
-    v.rows_per_block = S::kRB;
-    v.piece_units = S::kPieceUnits;
-    v.tma = true;
-    v.q_map = true;
-    return v;
-}
-
-template <typename T, bool kTicketMerge> bool pick_scored_tc5_variant(int D, bool paged, AttnVariant *v)
-{
-    switch (D) {
-    case 64:
-        *v = paged ? make_scored_tc5_variant<T, 64, kTicketMerge, true>() : make_scored_tc5_variant<T, 64, kTicketMerge, false>();
-        return true;
-    case 128:
-        *v = paged ? make_scored_tc5_variant<T, 128, kTicketMerge, true>() : make_scored_tc5_variant<T, 128, kTicketMerge, false>();
-        return true;
-    default: return false;
-    }
 }
 
 // The tcgen05 builds for one element type and merge mode: D = 64 or 128,

@@ -9,7 +9,7 @@
 //      row's state instead of an output (AttnScoredArgs::row_state);
 //   2. a prefix kernel over the B g N rows that each KV head has in the whole
 //      batch: a GEMM-shaped product that reads the prefix once (this file and
-//      kvd_prefix_tc5.cuh);
+//      kvd_pair_tc5.cuh);
 //   3. prefix_join_kernel: the join of a row's prefix pieces and own state.
 //
 // Rows of the prefix kernels.  A KV head's rows are those of its gN rows in
@@ -46,9 +46,8 @@ struct PrefixArgs {
     int slot_rows;                // unit_blocks * 128
     int page_shift, num_pages;
     float qscale;                 // softmax scale * log2(e)
-    int flags;
+    int flags;                    // (test builds: kArgTestStall)
 };
-constexpr int kPrefixTestStall = 1;  // (test builds only: see kArgTestStall)
 
 // First sequence and first of its rows of block k of a KV head.
 __device__ __forceinline__ int2 prefix_block_origin(const PrefixArgs &a, int k)
@@ -87,6 +86,7 @@ struct RowStateArgs {
     const int2 *seg;      // (first CTA, CTAs) per (b, h, row block)
     const int32_t *past_len;
     int rb, n_rowblocks, prow, T_max, max_past_len, N, grid;  // grid: the prefix kernel's CTAs
+    int pair_grid;              // > 0: part holds the pair kernel's slots (that many CTAs), rb 256
     int max_splits, cta_tiles;  // max_splits > 0: part holds the streaming kernel's slots [B * H_kv][max_splits][gN][D + 4]
 };
 
@@ -97,12 +97,58 @@ struct RowStateArgs {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBatch = 8;
 
+// Four columns of one row, joined part by part.
+template <int D> struct PieceJoin {
+    float M = -__builtin_huge_valf(), den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    __device__ __forceinline__ void add(float m, float l, const float4 &o)
+    {
+        const float Mn = fmaxf(M, m);
+        const float wa = safe_weight(M, Mn), wb = safe_weight(m, Mn);
+        den = den * wa + l * wb;
+        acc.x = acc.x * wa + o.x * wb;
+        acc.y = acc.y * wa + o.y * wb;
+        acc.z = acc.z * wa + o.z * wb;
+        acc.w = acc.w * wa + o.w * wb;
+        M = Mn;
+    }
+    // n pieces in slots slot_of(0), ... of [D / 4][rows] float4 and [2][rows]
+    // floats (m, l): row sr, column group c0.
+    template <typename F>
+    __device__ __forceinline__ void pieces(const float4 *part, const float *ml, int rows, int sr, int c0, int n, F slot_of)
+    {
+        for (int c = 0; c < n; c += kJoinBatch) {
+            float m[kJoinBatch], l[kJoinBatch];
+            float4 o[kJoinBatch];
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                const size_t slot = slot_of(min(c + i, n - 1));
+                m[i] = __ldcg(ml + slot * 2 * rows + sr);
+                l[i] = __ldcg(ml + (slot * 2 + 1) * rows + sr);
+                o[i] = __ldcg(part + (slot * (D / 4) + c0) * rows + sr);
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i)
+                if (c + i < n) add(m[i], l[i], o[i]);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void write(T *row) const
+    {
+        const float inv = den == 0.f ? 0.f : 1.f / den;  // (a row that sees nothing: zeros)
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4 *>(row) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        else
+            *reinterpret_cast<uint2 *>(row) =
+                make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv), pack_pair<T>(acc.z * inv, acc.w * inv));
+    }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixArgs a, const RowStateArgs s, void *out)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float kNegInf = __int_as_float(0xff800000);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int chunk = blockIdx.x % (kPrefixBlock / 32);
     const int gb = blockIdx.x / (kPrefixBlock / 32);  // block of all heads
@@ -118,55 +164,32 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
     const int2 seg = s.max_splits > 0 ? make_int2(0, 0) : __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
     if (!past_len_ok(P, s.N, s.T_max, s.max_past_len)) return;  // reported by the first launch
 
-    const long long n = (long long)a.n_units * a.n_tiles;
-    int first = 0, last = -1;  // CTAs that hold the unit's pieces (an empty prefix: none)
-    if (n > 0) {
-        first = owner_cta((long long)u * a.n_tiles, n, s.grid);
-        last = owner_cta((long long)(u + 1) * a.n_tiles - 1, n, s.grid);
-    }
-    float M = kNegInf, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float m, float l, const float4 &o) {
-        const float Mn = fmaxf(M, m);
-        const float wa = safe_weight(M, Mn), wb = safe_weight(m, Mn);
-        den = den * wa + l * wb;
-        acc.x = acc.x * wa + o.x * wb;
-        acc.y = acc.y * wa + o.y * wb;
-        acc.z = acc.z * wa + o.z * wb;
-        acc.w = acc.w * wa + o.w * wb;
-        M = Mn;
-    };
+    PieceJoin<D> j;
     // the row's own keys
-    const int own = s.max_splits > 0 ? stream_splits((P + s.N + 63) / 64, s.cta_tiles, s.max_splits) : seg.y;
-    for (int j = 0; j < own; ++j) {
-        const float *pr = s.max_splits > 0 ? s.part + (((size_t)bh * s.max_splits + j) * a.gN + p.y) * (D + 4)
-                          : seg.y == 1 ? s.state + ((size_t)bh * a.gN + p.y) * (D + 4)
-                                     : s.part + (((size_t)(seg.x + j) * 2 + (j == 0)) * s.prow + p.y % s.rb) * (D + 4);
-        const float4 o = __ldcg(reinterpret_cast<const float4 *>(pr) + c0);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pr + D));
-        add(ml.x, ml.y, o);
-    }
-    const float4 *part = reinterpret_cast<const float4 *>(a.part);
-    for (int c = first; c <= last; c += kJoinBatch) {
-        float m[kJoinBatch], l[kJoinBatch];
-        float4 o[kJoinBatch];
-#pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i) {
-            const size_t slot = (size_t)(u + min(c + i, last));
-            m[i] = __ldcg(a.part_ml + (slot * 2) * a.slot_rows + sr);
-            l[i] = __ldcg(a.part_ml + (slot * 2 + 1) * a.slot_rows + sr);
-            o[i] = __ldcg(part + (slot * (D / 4) + c0) * a.slot_rows + sr);
+    if (s.pair_grid > 0 && seg.y > 1) {
+        const int rows = a.gN > 128 ? 256 : 128;
+        j.pieces(reinterpret_cast<const float4 *>(s.part), s.part + (size_t)2 * s.pair_grid * rows * D, rows, p.y % 256, c0, seg.y,
+                 [&](int i) { return (size_t)(seg.x + i) * 2 + (i == 0 ? 1 : 0); });
+    } else {
+        const int own = s.max_splits > 0 ? stream_splits((P + s.N + 63) / 64, s.cta_tiles, s.max_splits) : seg.y;
+        for (int i = 0; i < own; ++i) {
+            const float *pr = s.max_splits > 0 ? s.part + (((size_t)bh * s.max_splits + i) * a.gN + p.y) * (D + 4)
+                              : seg.y == 1 ? s.state + ((size_t)bh * a.gN + p.y) * (D + 4)
+                                           : s.part + (((size_t)(seg.x + i) * 2 + (i == 0)) * s.prow + p.y % s.rb) * (D + 4);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(pr) + c0);
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pr + D));
+            j.add(ml.x, ml.y, o);
         }
-#pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i)
-            if (c + i <= last) add(m[i], l[i], o[i]);
     }
-    T *row = static_cast<T *>(out) + ((size_t)bh * a.gN + p.y) * D + c0 * 4;
-    const float inv = 1.f / den;
-    if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float4 *>(row) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    else
-        *reinterpret_cast<uint2 *>(row) = make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv), pack_pair<T>(acc.z * inv, acc.w * inv));
+    // the prefix's pieces: the CTAs that hold the unit's tiles (an empty prefix: none)
+    const long long n = (long long)a.n_units * a.n_tiles;
+    if (n > 0) {
+        const int first = owner_cta((long long)u * a.n_tiles, n, s.grid);
+        const int last = owner_cta((long long)(u + 1) * a.n_tiles - 1, n, s.grid);
+        j.pieces(reinterpret_cast<const float4 *>(a.part), a.part_ml, a.slot_rows, sr, c0, last - first + 1,
+                 [&](int i) { return (size_t)(u + first + i); });
+    }
+    j.template write<T>(static_cast<T *>(out) + ((size_t)bh * a.gN + p.y) * D + c0 * 4);
 }
 
 // Launch facts of a prefix kernel, for the host.
@@ -176,6 +199,14 @@ struct PrefixVariant {
     int threads, smem_bytes, tile_keys, join_grid_y;
     bool tma;  // takes the K, V and q tensor maps
 };
+
+// The pair kernel with modified scores (kvd_pair_tc5.cuh).
+struct PairVariant {
+    const void *fn, *join_fn;
+    int fixed_smem_bytes;  // plus 4 B + 1 ints
+};
+bool pair_variant_bf16(int D, bool paged, PairVariant *v);
+bool pair_variant_f16(int D, bool paged, PairVariant *v);
 
 bool prefix_variant_f32(int D, bool paged, PrefixVariant *v);
 bool prefix_variant_bf16(int D, bool paged, PrefixVariant *v);

@@ -113,7 +113,7 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     a.num_pages = paged != nullptr ? paged->num_pages : 0;
     a.qscale = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * kLog2e;
 #ifdef KVD_TIMEOUT_TEST
-    if (g_test_stall) a.flags = kPrefixTestStall;
+    if (g_test_stall) a.flags = kArgTestStall;
 #endif
     // (all that can be refused comes before the first launch)
     alignas(64) CUtensorMap tmk, tmv, tmv_last, tmq;
@@ -167,6 +167,7 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     s.rb = pl.own.rb;
     s.n_rowblocks = pl.own.n_rowblocks;
     s.prow = pl.own.prow;
+    s.pair_grid = pl.own.pair_grid;
     s.max_splits = pl.own.max_splits;
     s.cta_tiles = pl.own.cta_tiles;
     s.T_max = T_max;

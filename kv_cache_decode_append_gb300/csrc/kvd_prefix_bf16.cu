@@ -1,5 +1,5 @@
 // Instantiates the bf16 shared-prefix kernels (tcgen05) and their join.
-#include "kvd_prefix_tc5.cuh"
+#include "kvd_pair_tc5.cuh"
 
 namespace kvd {
 bool prefix_variant_bf16(int D, bool paged, PrefixVariant *v) { return pick_prefix_tc5<__nv_bfloat16>(D, paged, v); }

@@ -1,10 +1,6 @@
-// Instantiates the f16 tcgen05 attention kernels with modified scores (RB 128),
-// the separate merge pass.
-#include "kvd_attention_tc5.cuh"
+// Instantiates the f16 tcgen05 kernels with modified scores and their join.
+#include "kvd_pair_tc5.cuh"
 
 namespace kvd {
-bool attn_variant_scored_f16(int D, int RB, bool paged, AttnVariant *v)
-{
-    return RB == 128 && pick_scored_tc5_variant<__half, false>(D, paged, v);
-}
+bool pair_variant_f16(int D, bool paged, PairVariant *v) { return pick_pair_scored<__half>(D, paged, v); }
 }  // namespace kvd

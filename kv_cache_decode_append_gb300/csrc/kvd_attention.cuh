@@ -156,18 +156,6 @@ __device__ __forceinline__ bool row_sees(const RowScore &r, int pre, int key)
     return key >= r.doc && (key < pre || (key >= r.lo && key <= r.p));
 }
 
-// Two scores capped as below with one reciprocal: 1 / a and 1 / b from 1 / (a b)
-// (the exponents limited to 2^60: tanh is 1 in fp32 from 2^26 on).
-__device__ __forceinline__ void cap_score_pair(float &y0, float &y1, float C, float cap_in)
-{
-    const float e0 = 1.f + fast_exp2(fminf(y0 * cap_in, 60.f)), e1 = 1.f + fast_exp2(fminf(y1 * cap_in, 60.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e0 * e1));
-    r *= -2.f * C;
-    y0 = fmaf(r, e1, C);
-    y1 = fmaf(r, e0, C);
-}
-
 // C tanh(y0 / C).  For 16-bit results tanh z = 1 - 2 / (1 + e^2z) with the
 // approximate exp2 and reciprocal: off by at most about 2^-21 absolutely, which
 // moves a weight by C 2^-21 relatively (cap 50: 3e-5, a hundredth of a bf16

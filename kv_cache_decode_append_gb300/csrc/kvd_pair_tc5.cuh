@@ -96,6 +96,18 @@ __device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// tcgen05.st of 16 consecutive 32-bit columns of this thread's lane, waited for.
+__device__ __forceinline__ void tc5_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n"
+        "tcgen05.wait::st.sync.aligned;\n"
+        :
+        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // One thread of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -180,6 +192,18 @@ template <typename T, int D, bool kPaged> struct PrefixJob {
         }
     }
     __device__ void begin(int, int) {}
+    __device__ __forceinline__ void scores(uint32_t (&s)[32], int c, bool) const
+    {
+        const int left = a.S - (k * 128 + c * 32);
+        if (left < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i >= left) s[i] = 0xff800000u;  // -inf
+        }
+    }
+    __device__ bool maximum_modified() const { return false; }
+    __device__ float maximum(float top) const { return top * a.qscale; }
+    __device__ float exponent_scale() const { return a.qscale; }
     // Row r of block x: its piece's state, columns c0 .. c0 + 31 of o at a time.
     __device__ void store(int x, int r, int c0, const uint32_t (&o)[32], float m, float l) const
     {
@@ -381,34 +405,53 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
             ml[rows] = l;
         }
     }
-    // The half's scores modified (log2 units where anything but bounds applies,
-    // else still raw) and bounded.
-    __device__ void scores(uint32_t (&s)[64], int half) const
+    // Columns 32 c .. 32 c + 31 of the tile's raw scores, bounded (-inf), and
+    // with `modify` modified first (to log2 units; a cap alone keeps the order of
+    // scores, so a row's maximum is capped rather than its scores).
+    __device__ __forceinline__ void scores(uint32_t (&s)[32], int c, bool modify) const
     {
-        const int base = key(half);
-        if (a.cap > 0.f) {
+        const int half = c / 2, base = key(half) + (c % 2) * 32;
+        if (modify) {
+            if (a.cap > 0.f) {
+                const float in = a.qscale * a.cap_in;
+                const f32x2 in2 = pack2(in, in), one2 = pack2(1.f, 1.f), c2 = pack2(a.cap, a.cap);
+                // (cap_score for two with one reciprocal: 1 / a and 1 / b from
+                // 1 / (a b), the exponents limited to 2^60, where tanh is 1)
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                float y0 = __uint_as_float(s[c]) * a.qscale, y1 = __uint_as_float(s[c + 1]) * a.qscale;
-                cap_score_pair(y0, y1, a.cap, a.cap_in);
-                s[c] = __float_as_uint(y0);
-                s[c + 1] = __float_as_uint(y1);
+                for (int i = 0; i < 32; i += 2) {
+                    float x0, x1;
+                    unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), in2), x0, x1);
+                    const f32x2 e = add2(pack2(fast_exp2(fminf(x0, 60.f)), fast_exp2(fminf(x1, 60.f))), one2);
+                    float e0, e1, r;
+                    unpack2(e, e0, e1);
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e0 * e1));
+                    r *= -2.f * a.cap;
+                    unpack2(fma2(pack2(r, r), pack2(e1, e0), c2), x0, x1);
+                    s[i] = __float_as_uint(x0);
+                    s[i + 1] = __float_as_uint(x1);
+                }
             }
-        } else if (a.slopes != nullptr) {
+            if (a.slopes != nullptr) {
+                const float d0 = (float)(rs.p - base), q = a.cap > 0.f ? 1.f : a.qscale;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * a.qscale);
+                for (int i = 0; i < 32; ++i)  // (whole numbers: d0 - i is exact below 2^24)
+                    s[i] = __float_as_uint(fmaf(-rs.slope, fabsf(d0 - (float)i), __uint_as_float(s[i]) * q));
+            }
         }
-        if (a.slopes != nullptr) {
-            const float d0 = (float)(rs.p - base);  // (whole numbers: d0 - c is exact below 2^24)
-#pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = __float_as_uint(fmaf(-rs.slope, fabsf(d0 - (float)c), __uint_as_float(s[c])));
-        }
-        if (!has(half) || base + 64 > k_end() || !row_sees_all<64>(rs, mod.pre, base)) {
+        if (!has(half) || base + 32 > k_end() || !row_sees_all<32>(rs, mod.pre, base)) {
             const int end = has(half) ? k_end() : base;
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                if (base + c >= end || !row_sees(rs, mod.pre, base + c)) s[c] = 0xff800000u;
+            for (int i = 0; i < 32; ++i)
+                if (base + i >= end || !row_sees(rs, mod.pre, base + i)) s[i] = 0xff800000u;
         }
+    }
+    // Whether a maximum has to be taken over modified scores; a raw maximum in
+    // log2 units; what the exponents multiply the scores by.
+    __device__ bool maximum_modified() const { return a.slopes != nullptr; }
+    __device__ float maximum(float top) const
+    {
+        if (a.slopes != nullptr || top == __int_as_float(0xff800000)) return top;
+        return a.cap > 0.f ? cap_score<false>(top * a.qscale, a.cap, a.cap_in) : top * a.qscale;
     }
     // Whether value row r of the tile must be zeroed.
     __device__ bool some_zero() const
@@ -688,57 +731,38 @@ __global__ void __launch_bounds__(320, 1)
                     break;
                 }
                 tc5_fence_after();
-                uint32_t s0[64], s1[64];
-                tc5_ld64(t_s, s0);
-                tc5_ld64(t_s + 64, s1);
-                float escale = a.qscale;
-                if constexpr (Job::kMod) {
-                    job.scores(s0, 0);
-                    job.scores(s1, 1);
-                    escale = job.exponent_scale();
-                } else {
-                    const int nk = job.k_end() - job.key(0);
-                    if (nk < S::kTK) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) {
-                            if (c >= nk) s0[c] = 0xff800000u;  // -inf
-                            if (64 + c >= nk) s1[c] = 0xff800000u;
-                        }
-                    }
-                }
-                // (four chains of three-input maxima)
-                float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-                for (int c = 0; c < 64; ++c) mx[c & 3] = max3(mx[c & 3], __uint_as_float(s0[c]), __uint_as_float(s1[c]));
-                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * escale;
                 float alpha = 1.f;
                 bool rescale = false;
-                if (top > m_run + kRescaleThreshold) {
-                    if (!first) {
-                        alpha = fast_exp2(m_run - top);
-                        rescale = true;
+                // A maximum that grew by more than 2^8: O follows (rows that keep
+                // their maximum scale by 1).
+                auto raise = [&](float top) {
+                    if (top > m_run + kRescaleThreshold) {
+                        if (!first) {
+                            alpha = fast_exp2(m_run - top);
+                            rescale = true;
+                        }
+                        m_run = top;
                     }
-                    m_run = top;
-                }
-                if (__any_sync(0xffffffffu, rescale)) {  // (rows that keep their max scale by 1)
+                    if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t o[32];
-                        tc5_ld32(t_o + c0, o);
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tc5_ld32(t_o + c0, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tc5_st32(t_o + c0, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tc5_st32(t_o + c0, o);
+                        }
                     }
-                }
-                // weights 2^(qscale s - m): scale and maximum in one packed FMA,
+                };
+                // weights 2^(escale s - m): scale and maximum in one packed FMA,
                 // sums as packed pairs in four chains
-                const float nmu = (m_run == kNegInf) ? 0.f : -m_run;
-                const f32x2 q2 = pack2(escale, escale), nmu2 = pack2(nmu, nmu);
                 f32x2 l4[4] = {0ull, 0ull, 0ull, 0ull};
-                uint32_t pk[32];
-                auto weights = [&](const uint32_t (&s)[64]) {
+                auto weights = [&](const auto &s, auto &pk, float escale) {
+                    constexpr int n = sizeof(pk) / sizeof(pk[0]);
+                    const float nmu = (m_run == kNegInf) ? 0.f : -m_run;
+                    const f32x2 q2 = pack2(escale, escale), nmu2 = pack2(nmu, nmu);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
+                    for (int c = 0; c < n; ++c) {
                         float y0, y1;
                         unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), q2, nmu2), y0, y1);
                         const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
@@ -746,10 +770,30 @@ __global__ void __launch_bounds__(320, 1)
                         pk[c] = pack_pair<T>(p0, p1);
                     }
                 };
-                weights(s0);
-                tc5_st32(t_s, pk);
-                weights(s1);
-                tc5_st32(t_s + 32, pk);
+                // 32 columns at a time and rolled: over the whole tile, the scores
+                // alone are 128 registers, and modified scores' code is more than
+                // the instruction cache holds (@@).
+                float mx = kNegInf;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t s[32];
+                    tc5_ld32(t_s + 32 * c, s);
+                    job.scores(s, c, job.maximum_modified());
+                    float m4[4] = {mx, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                    mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+                }
+                raise(job.maximum(mx));
+                const float escale = job.exponent_scale();
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {  // (weights 32 c .. over columns that are read)
+                    uint32_t s[32], pk[16];
+                    tc5_ld32(t_s + 32 * c, s);
+                    job.scores(s, c, true);
+                    weights(s, pk, escale);
+                    tc5_st16(t_s + 16 * c, pk);
+                }
                 float le, lo2;
                 unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), le, lo2);
                 l_run = l_run * alpha + (le + lo2);

@@ -512,7 +512,9 @@ kvd_status kvd_paged_rope_append(const void *q, void *q_out, void *k_pages, void
  *   workspace   of at least kvd_decode_scored_workspace_bytes(...) bytes,
  *               otherwise as for kvd_decode_attention
  * fp32, bf16 and fp16; other arguments, limits, errors and device-side checks as
- * for the plain calls.  softcap negative, infinite or NaN, or window negative:
+ * for the plain calls.  fp32, and 16-bit dtypes with more than 16 query rows per
+ * KV head, hold 2048 sequences and more, but not any number: more than the SM's
+ * shared memory can list are KVD_ERR_UNSUPPORTED.  softcap negative, infinite or NaN, or window negative:
  * KVD_ERR_INVALID_ARG.  16-bit dtypes take tanh as 1 - 2 / (1 + e^2x) with
  * approximate exponential and reciprocal (off by about 2^-21 softcap).
  */
@@ -560,7 +562,7 @@ kvd_status kvd_paged_decode_attention_scored(const void *q, const void *k_pages,
  *                       Calls that run concurrently need distinct workspaces.
  * Rows past prefix_len may hold anything.  Other arguments, limits, errors and
  * device-side checks as for kvd_decode_attention (kvd_paged_decode_attention):
- * (H_q / H_kv) * N <= 1024 rows per sequence, any B.  prefix_len > S_max, or more
+ * (H_q / H_kv) * N <= 1024 rows per sequence, B as for the scored calls.  prefix_len > S_max, or more
  * prefix pages than the pool has: KVD_ERR_CAPACITY.  Positions for a model that
  * rotates: kvd_rope_append with pos_base = prefix_len.
  */

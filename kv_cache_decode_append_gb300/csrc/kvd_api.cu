@@ -466,6 +466,7 @@ kvd_status make_stream_plan(int B, int H_kv, int D, int N, int max_past_len, kvd
     per = std::min<long long>(std::max<long long>((per + 3) / 4 * 4, 4), std::max<long long>(tiles, 4));
     pl->sms = sms;
     pl->cta_tiles = (int)per;
+    pl->grid = 0;  // (from heads and splits)
     pl->max_splits = (int)std::max<long long>((tiles + per - 1) / per, 1);
     pl->stream_fn = dtype == KVD_BF16 ? stream_kernel_bf16(D, pl->rows, paged) : stream_kernel_f16(D, pl->rows, paged);
     pl->early = pl->merge_pass = false;
@@ -1012,7 +1013,8 @@ kvd_status decode_launch(const void *q, const void *k_cache, const void *v_cache
         cfg.gridDim = dim3((unsigned)std::max<long long>(ctas, 1));
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelExC(&cfg, pl.v.merge_fn, args) != cudaSuccess) return KVD_ERR_CUDA;
+        void *margs[] = {&a, &pl.grid};
+        if (cudaLaunchKernelExC(&cfg, pl.v.merge_fn, margs) != cudaSuccess) return KVD_ERR_CUDA;
     }
     return KVD_OK;
 }
@@ -1034,6 +1036,7 @@ kvd_status row_state_plan(int B, int H_q, int H_kv, int D, int N, int max_past_l
     plan->pair_grid = pl.pair ? pl.grid : 0;
     plan->max_splits = pl.stream_fn != nullptr ? pl.max_splits : 0;
     plan->cta_tiles = pl.cta_tiles;
+    plan->grid = pl.grid;
     plan->part_off = pl.part_off;
     plan->seg_off = pl.seg_off;
     plan->state_off = pl.state_off;

@@ -1556,12 +1556,12 @@ __global__ void __launch_bounds__(AttnShape<T, D, RB, C>::kThreads)
 // so the host may launch fewer warps than rows.  A warp takes one row at a
 // time when the grid has a warp per row, else kMergeRows consecutive rows of
 // one head with the loads of all of them in flight together (a row alone is
-// two dependent memory round trips).  Measured on GB300 (long-context layer):
+// two dependent memory round trips).  n_ctas: the split pass's CTAs.  Measured on GB300 (long-context layer):
 // one row per warp is best at 1024 rows, two at 8192 and 32768 rows.
 constexpr int kMergeRows = 2;
 
 template <typename T, int D, int RB, bool kScaleV = false, bool kMod = false>
-__global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a, const int n_ctas)
 {
     using Ty = Elem<T>;
     const float kNegInf = __int_as_float(0xff800000);
@@ -1596,7 +1596,8 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a)
         int cnt[kR], kmax = 0;
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
-            cnt[i] = seg[i].y > 1 ? seg[i].y : 0;
+            // (no such CTAs: not written, as a CTA gave up)
+            cnt[i] = seg[i].y > 1 && seg[i].x >= 0 && seg[i].y <= n_ctas - seg[i].x ? seg[i].y : 0;
             kmax = max(kmax, cnt[i]);
         }
         if (kmax == 0) continue;

@@ -231,136 +231,136 @@ __global__ void __launch_bounds__(128, StreamShape<D, NR>::kCtas) attn_stream_ke
         __syncwarp();
         const int tile0 = reg.tile(tc) * S::kTK, keys_here = min(S::kTK, k_end - tile0);
 #pragma unroll
-      for (int half = 0; half < S::kStep / 16; ++half) {
-        const int in_tile = subc * S::kStep + half * 16, key0 = tile0 + in_tile;
-        const uint32_t kd = ring + st * 2 * S::kHalf + half * 16 * kRowBytes, vd = kd + S::kHalf;
-        uint4 kf[2][kKb];
+        for (int half = 0; half < S::kStep / 16; ++half) {
+            const int in_tile = subc * S::kStep + half * 16, key0 = tile0 + in_tile;
+            const uint32_t kd = ring + st * 2 * S::kHalf + half * 16 * kRowBytes, vd = kd + S::kHalf;
+            uint4 kf[2][kKb];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < kKb; ++j)
-                kf[i][j] = lds128_addr(kd + (g + 8 * i) * kRowBytes + (((4 * j + t) ^ ((g & 1) << 2)) << 4));
+                for (int j = 0; j < kKb; ++j)
+                    kf[i][j] = lds128_addr(kd + (g + 8 * i) * kRowBytes + (((4 * j + t) ^ ((g & 1) << 2)) << 4));
 
-        // ---- S^T = K Q^T: even and odd k-steps in two chains ----
-        float s[NR][4], s2[NR][4];
+            // ---- S^T = K Q^T: even and odd k-steps in two chains ----
+            float s[NR][4], s2[NR][4];
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kKb; ++j) {
-            const uint32_t a0[4] = {kf[0][j].x, kf[1][j].x, kf[0][j].y, kf[1][j].y};
-            const uint32_t a1[4] = {kf[0][j].z, kf[1][j].z, kf[0][j].w, kf[1][j].w};
+            for (int j = 0; j < kKb; ++j) {
+                const uint32_t a0[4] = {kf[0][j].x, kf[1][j].x, kf[0][j].y, kf[1][j].y};
+                const uint32_t a1[4] = {kf[0][j].z, kf[1][j].z, kf[0][j].w, kf[1][j].w};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    mma_16816<T>(s[n], a0, q[n][j].x, q[n][j].y);
+                    mma_16816<T>(s2[n], a1, q[n][j].z, q[n][j].w);
+                }
+            }
+            // ---- scores (log2 units), bounds ----
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s2[n][e]) * a.qscale;
+            if (a.cap > 0.f) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] = cap_score<false>(s[n][e], a.cap, a.cap_in);
+            }
+            if (a.slopes != nullptr) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {  // (whole numbers: exact below 2^24)
+                        const float d = (float)(rs[n][e].p - key0 - g);
+                        s[n][e] = fmaf(-rs[n][e].slope, fabsf(d), s[n][e]);
+                        s[n][e + 2] = fmaf(-rs[n][e].slope, fabsf(d - 8.f), s[n][e + 2]);
+                    }
+            }
+            const bool masked = in_tile + 16 > keys_here || !row_sees_all<16>(every, mod.pre, key0);  // (warp-uniform)
+            if (masked) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + g + 8 * (e >> 1);
+                        if (key >= k_end || !row_sees(rs[n][e & 1], mod.pre, key)) s[n][e] = kNegInf;
+                    }
+            }
+
+            // ---- online softmax per query row 2t + (e & 1) ----
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) grow = grow || s[n][e] > m[n][e & 1] + kRescaleThreshold;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mt = fmaxf(s[n][e], s[n][e + 2]);
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+                        if (mt > m[n][e] + kRescaleThreshold) {
+                            const float alpha = fast_exp2(m[n][e] - mt);
+                            l[n][e] *= alpha;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                o[n][i][e] *= alpha;
+                                o[n][i][e + 2] *= alpha;
+                            }
+                            m[n][e] = mu[n][e] = mt;
+                        }
+                    }
+            }
+            uint32_t pb[NR][2];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                mma_16816<T>(s[n], a0, q[n][j].x, q[n][j].y);
-                mma_16816<T>(s2[n], a1, q[n][j].z, q[n][j].w);
-            }
-        }
-        // ---- scores (log2 units), bounds ----
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s2[n][e]) * a.qscale;
-        if (a.cap > 0.f) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = cap_score<false>(s[n][e], a.cap, a.cap_in);
-        }
-        if (a.slopes != nullptr) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {  // (whole numbers: exact below 2^24)
-                    const float d = (float)(rs[n][e].p - key0 - g);
-                    s[n][e] = fmaf(-rs[n][e].slope, fabsf(d), s[n][e]);
-                    s[n][e + 2] = fmaf(-rs[n][e].slope, fabsf(d - 8.f), s[n][e + 2]);
-                }
-        }
-        const bool masked = in_tile + 16 > keys_here || !row_sees_all<16>(every, mod.pre, key0);  // (warp-uniform)
-        if (masked) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int key = key0 + g + 8 * (e >> 1);
-                    if (key >= k_end || !row_sees(rs[n][e & 1], mod.pre, key)) s[n][e] = kNegInf;
+                    s[n][e] = fast_exp2(s[n][e] - mu[n][e & 1]);
+                    l[n][e & 1] += s[n][e];
                 }
-        }
-
-        // ---- online softmax per query row 2t + (e & 1) ----
-        bool grow = false;
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) grow = grow || s[n][e] > m[n][e & 1] + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mt = fmaxf(s[n][e], s[n][e + 2]);
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                    if (mt > m[n][e] + kRescaleThreshold) {
-                        const float alpha = fast_exp2(m[n][e] - mt);
-                        l[n][e] *= alpha;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            o[n][i][e] *= alpha;
-                            o[n][i][e + 2] *= alpha;
-                        }
-                        m[n][e] = mu[n][e] = mt;
-                    }
-                }
-        }
-        uint32_t pb[NR][2];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[n][e] = fast_exp2(s[n][e] - mu[n][e & 1]);
-                l[n][e & 1] += s[n][e];
+                pb[n][0] = movmatrix_trans(pack_pair<T>(s[n][0], s[n][1]));
+                pb[n][1] = movmatrix_trans(pack_pair<T>(s[n][2], s[n][3]));
             }
-            pb[n][0] = movmatrix_trans(pack_pair<T>(s[n][0], s[n][1]));
-            pb[n][1] = movmatrix_trans(pack_pair<T>(s[n][2], s[n][3]));
-        }
 
-        uint4 vf[4][kVb];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-            for (int c = 0; c < kVb; ++c) vf[i][c] = lds128_addr(vd + r * kRowBytes + (((8 * c + g) ^ (r & 6)) << 4));
-        }
-        // ---- value rows that no row of the sequence sees: zero ----
-        if (masked && some_unseen(mod, key0, 16, k_end)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (key_unseen(mod, key0 + 2 * t + (i & 1) + 8 * (i >> 1), k_end)) {
-#pragma unroll
-                    for (int c = 0; c < kVb; ++c) vf[i][c] = make_uint4(0u, 0u, 0u, 0u);
-                }
-        }
-
-        // ---- O^T += V^T P^T ----
-#pragma unroll
-        for (int c = 0; c < kVb; ++c) {
-            const uint32_t w[4][4] = {{vf[0][c].x, vf[0][c].y, vf[0][c].z, vf[0][c].w},
-                                      {vf[1][c].x, vf[1][c].y, vf[1][c].z, vf[1][c].w},
-                                      {vf[2][c].x, vf[2][c].y, vf[2][c].z, vf[2][c].w},
-                                      {vf[3][c].x, vf[3][c].y, vf[3][c].z, vf[3][c].w}};
+            uint4 vf[4][kVb];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t va[4] = {__byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
-                                        __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632)};
+                const int r = 2 * t + (i & 1) + 8 * (i >> 1);
 #pragma unroll
-                for (int n = 0; n < NR; ++n) mma_16816<T>(o[n][4 * c + i], va, pb[n][0], pb[n][1]);
+                for (int c = 0; c < kVb; ++c) vf[i][c] = lds128_addr(vd + r * kRowBytes + (((8 * c + g) ^ (r & 6)) << 4));
+            }
+            // ---- value rows that no row of the sequence sees: zero ----
+            if (masked && some_unseen(mod, key0, 16, k_end)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (key_unseen(mod, key0 + 2 * t + (i & 1) + 8 * (i >> 1), k_end)) {
+#pragma unroll
+                        for (int c = 0; c < kVb; ++c) vf[i][c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+            }
+
+            // ---- O^T += V^T P^T ----
+#pragma unroll
+            for (int c = 0; c < kVb; ++c) {
+                const uint32_t w[4][4] = {{vf[0][c].x, vf[0][c].y, vf[0][c].z, vf[0][c].w},
+                                          {vf[1][c].x, vf[1][c].y, vf[1][c].z, vf[1][c].w},
+                                          {vf[2][c].x, vf[2][c].y, vf[2][c].z, vf[2][c].w},
+                                          {vf[3][c].x, vf[3][c].y, vf[3][c].z, vf[3][c].w}};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t va[4] = {__byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
+                                            __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632)};
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma_16816<T>(o[n][4 * c + i], va, pb[n][0], pb[n][1]);
+                }
             }
         }
-      }
         __syncwarp();  // (the step is read: the next copy may overwrite it)
         if (++st == S::kDepth) st = 0;
         if (++subc * S::kStep >= keys_here) {

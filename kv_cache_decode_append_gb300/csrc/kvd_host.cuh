@@ -42,6 +42,7 @@ struct RowStatePlan {
     int rb, n_rowblocks, prow;  // rows per block, blocks per head, rows per piece slot
     int pair_grid;              // > 0: the pair kernel's CTAs (rb 256) ...
     int max_splits, cta_tiles;  // ... max_splits > 0: the streaming kernel's slots per head, and their tiles, instead
+    int grid;                   // its CTAs
     size_t part_off, seg_off, state_off, bytes;
 };
 kvd_status row_state_plan(int B, int H_q, int H_kv, int D, int N, int max_past_len, kvd_dtype dtype, bool paged,

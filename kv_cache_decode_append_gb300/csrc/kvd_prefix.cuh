@@ -86,6 +86,7 @@ struct RowStateArgs {
     const int2 *seg;      // (first CTA, CTAs) per (b, h, row block)
     const int32_t *past_len;
     int rb, n_rowblocks, prow, T_max, max_past_len, N, grid;  // grid: the prefix kernel's CTAs
+    int own_grid;               // the attention kernel's CTAs (a bound on seg)
     int pair_grid;              // > 0: part holds the pair kernel's slots (that many CTAs), rb 256
     int max_splits, cta_tiles;  // max_splits > 0: part holds the streaming kernel's slots [B * H_kv][max_splits][gN][D + 4]
 };
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
     const int P = __ldg(s.past_len + p.x);
     const int2 seg = s.max_splits > 0 ? make_int2(0, 0) : __ldcg(s.seg + (size_t)bh * s.n_rowblocks + p.y / s.rb);
     if (!past_len_ok(P, s.N, s.T_max, s.max_past_len)) return;  // reported by the first launch
+    if (s.max_splits == 0 && (seg.x < 0 || seg.y > s.own_grid - seg.x)) return;  // (not written: a CTA gave up)
 
     PieceJoin<D> j;
     // the row's own keys

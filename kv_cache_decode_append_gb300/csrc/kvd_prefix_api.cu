@@ -174,6 +174,7 @@ kvd_status prefix_launch(const void *q, const void *k_prefix, const void *v_pref
     s.max_past_len = max_past_len;
     s.N = N;
     s.grid = pl.grid;
+    s.own_grid = pl.own.grid;
     cfg.gridDim = dim3((unsigned)(H_kv * pl.blocks * (kPrefixBlock / 32)), (unsigned)pl.v.join_grid_y);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;

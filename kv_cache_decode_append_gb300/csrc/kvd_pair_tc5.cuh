@@ -96,12 +96,40 @@ __device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
-// tcgen05.st of 16 consecutive 32-bit columns of this thread's lane, waited for.
+// A pair of weights times a factor.
+template <typename T> __device__ __forceinline__ uint32_t scale_pair(uint32_t w, float f)
+{
+    float lo, hi;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        lo = v.x;
+        hi = v.y;
+    }
+    return pack_pair<T>(lo * f, hi * f);
+}
+
+// tcgen05.ld of 16 consecutive 32-bit columns of this thread's lane, waited for.
+__device__ __forceinline__ void tc5_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// tcgen05.st of 16 consecutive 32-bit columns of this thread's lane; not waited
+// for (tc5_st_wait).
+__device__ __forceinline__ void tc5_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc5_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n"
-        "tcgen05.wait::st.sync.aligned;\n"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
         :
         : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
           "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
@@ -192,6 +220,7 @@ template <typename T, int D, bool kPaged> struct PrefixJob {
         }
     }
     __device__ void begin(int, int) {}
+    __device__ void tile() {}
     __device__ __forceinline__ void scores(uint32_t (&s)[32], int c, bool) const
     {
         const int left = a.S - (k * 128 + c * 32);
@@ -253,6 +282,8 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
     // softmax warps: the row's bounds, its sequence's
     RowScore rs;
     ModTile mod;
+    int key0, key1;
+    bool open;
 
     // One warp: pre[b] = cost of sequences 0 .. b-1 per unit, pl[b] = P_b, then
     // the sequences' first document keys and prefix lengths.
@@ -405,16 +436,24 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
             ml[rows] = l;
         }
     }
+    // A tile starts: its halves' keys, and whether the row sees all of them.
+    __device__ void tile()
+    {
+        key0 = key(0);
+        key1 = key(1);
+        open = has(1) && max(key0, key1) + 64 <= k_end() && row_sees_all<64>(rs, mod.pre, key0) &&
+               row_sees_all<64>(rs, mod.pre, key1);
+    }
     // Columns 32 c .. 32 c + 31 of the tile's raw scores, bounded (-inf), and
     // with `modify` modified first (to log2 units; a cap alone keeps the order of
     // scores, so a row's maximum is capped rather than its scores).
     __device__ __forceinline__ void scores(uint32_t (&s)[32], int c, bool modify) const
     {
-        const int half = c / 2, base = key(half) + (c % 2) * 32;
+        const int half = c / 2, base = (half == 0 ? key0 : key1) + (c % 2) * 32;
         if (modify) {
             if (a.cap > 0.f) {
                 const float in = a.qscale * a.cap_in;
-                const f32x2 in2 = pack2(in, in), one2 = pack2(1.f, 1.f), c2 = pack2(a.cap, a.cap);
+                const f32x2 in2 = pack2(in, in), one2 = pack2(1.f, 1.f);
                 // (cap_score for two with one reciprocal: 1 / a and 1 / b from
                 // 1 / (a b), the exponents limited to 2^60, where tanh is 1)
 #pragma unroll
@@ -426,9 +465,8 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
                     unpack2(e, e0, e1);
                     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e0 * e1));
                     r *= -2.f * a.cap;
-                    unpack2(fma2(pack2(r, r), pack2(e1, e0), c2), x0, x1);
-                    s[i] = __float_as_uint(x0);
-                    s[i + 1] = __float_as_uint(x1);
+                    s[i] = __float_as_uint(fmaf(r, e1, a.cap));
+                    s[i + 1] = __float_as_uint(fmaf(r, e0, a.cap));
                 }
             }
             if (a.slopes != nullptr) {
@@ -438,7 +476,7 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
                     s[i] = __float_as_uint(fmaf(-rs.slope, fabsf(d0 - (float)i), __uint_as_float(s[i]) * q));
             }
         }
-        if (!has(half) || base + 32 > k_end() || !row_sees_all<32>(rs, mod.pre, base)) {
+        if (!open) {
             const int end = has(half) ? k_end() : base;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -499,6 +537,7 @@ __global__ void __launch_bounds__(320, 1)
     using S = PairTc5Shape<D, Job::kSlots>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kRescaleThreshold = 8.0f;
+    constexpr float kLateLimit = kBf16 ? 24.0f : 15.0f;  // (fp16 weights end at 2^16)
     const float kNegInf = __int_as_float(0xff800000);
     extern __shared__ __align__(1024) unsigned char smem_pair[];
     unsigned char *smem = smem_pair;
@@ -713,7 +752,8 @@ __global__ void __launch_bounds__(320, 1)
         const int x = warp / 4, r = tid % 128;
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t t_s = tmem + lanes + S::kTmemS + x * 128, t_o = tmem + lanes + S::kTmemO + x * D;
-        float m_run = kNegInf, l_run = 0.f;
+        // m_run: what the exponents subtract; m_seen: the row's true maximum so far
+        float m_run = kNegInf, m_seen = kNegInf, l_run = 0.f;
         uint32_t n_s = 0u;
         bool dead = false;
         auto warp_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -724,82 +764,98 @@ __global__ void __launch_bounds__(320, 1)
             if (x < job.blocks_here()) {
                 if (first) {
                     job.begin(x, r);
-                    m_run = kNegInf;
+                    m_run = m_seen = kNegInf;
                     l_run = 0.f;
                 }
+                job.tile();
                 if (!warp_wait(&s_full[x], n_s)) {
                     dead = true;
                     break;
                 }
                 tc5_fence_after();
-                float alpha = 1.f;
-                bool rescale = false;
-                // A maximum that grew by more than 2^8: O follows (rows that keep
-                // their maximum scale by 1).
-                auto raise = [&](float top) {
-                    if (top > m_run + kRescaleThreshold) {
-                        if (!first) {
-                            alpha = fast_exp2(m_run - top);
-                            rescale = true;
-                        }
-                        m_run = top;
-                    }
-                    if (__any_sync(0xffffffffu, rescale)) {
+                // O, the sum and the maximum move to a larger maximum (rows that
+                // keep theirs: by a factor of 1).
+                auto raise = [&](bool grows, float to) {
+                    if (!__any_sync(0xffffffffu, grows)) return;
+                    const float alpha = grows ? fast_exp2(m_run - to) : 1.f;
+                    if (grows) m_run = to;
+                    l_run *= alpha;
+                    if (first) return;  // (no O yet)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tc5_ld32(t_o + c0, o);
 #pragma unroll
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tc5_ld32(t_o + c0, o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tc5_st32(t_o + c0, o);
-                        }
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tc5_st32(t_o + c0, o);
                     }
                 };
-                // weights 2^(escale s - m): scale and maximum in one packed FMA,
-                // sums as packed pairs in four chains
-                f32x2 l4[4] = {0ull, 0ull, 0ull, 0ull};
-                auto weights = [&](const auto &s, auto &pk, float escale) {
-                    constexpr int n = sizeof(pk) / sizeof(pk[0]);
-                    const float nmu = (m_run == kNegInf) ? 0.f : -m_run;
-                    const f32x2 q2 = pack2(escale, escale), nmu2 = pack2(nmu, nmu);
+                auto chunk_max = [&](const uint32_t (&s)[32]) -> float {
+                    float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                    for (int c = 0; c < n; ++c) {
-                        float y0, y1;
-                        unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), q2, nmu2), y0, y1);
-                        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-                        l4[c & 3] = add2(l4[c & 3], pack2(p0, p1));
-                        pk[c] = pack_pair<T>(p0, p1);
-                    }
+                    for (int i = 0; i < 32; i += 2) m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                    return max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                 };
                 // 32 columns at a time and rolled: over the whole tile, the scores
                 // alone are 128 registers, and modified scores' code outgrows the
                 // instruction cache (a capped 128-token chunk 118 us unrolled, 91
                 // rolled; a prefix of 16384 keys for 128 sequences 70 and 72).
                 // Sixteen softmax warps, two threads a row: 90 and 71 us.
-                float mx = kNegInf;
+                if (__any_sync(0xffffffffu, m_run == kNegInf)) {
+                    float mx = kNegInf;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32];
-                    tc5_ld32(t_s + 32 * c, s);
-                    job.scores(s, c, job.maximum_modified());
-                    float m4[4] = {mx, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-                    mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32];
+                        tc5_ld32(t_s + 32 * c, s);
+                        job.scores(s, c, job.maximum_modified());
+                        mx = fmaxf(mx, chunk_max(s));
+                    }
+                    m_seen = fmaxf(m_seen, job.maximum(mx));
                 }
-                raise(job.maximum(mx));
+                raise(m_seen > m_run + kRescaleThreshold, m_seen);
                 const float escale = job.exponent_scale();
+                float l_tile = 0.f;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {  // (weights 32 c .. over columns that are read)
                     uint32_t s[32], pk[16];
                     tc5_ld32(t_s + 32 * c, s);
                     job.scores(s, c, true);
-                    weights(s, pk, escale);
+                    const float top = chunk_max(s) * escale;
+                    m_seen = fmaxf(m_seen, top);
+                    if (const bool late = top > m_run + kLateLimit; __any_sync(0xffffffffu, late)) {
+                        // by a power of two: the weights that are written scale exactly
+                        const float to = late ? m_run + floorf(top - m_run) : m_run;
+                        const float alpha = late ? fast_exp2(m_run - to) : 1.f;
+                        l_tile *= alpha;
+                        tc5_st_wait();
+                        for (int w = 0; w < c; ++w) {
+                            tc5_ld16(t_s + 16 * w, pk);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pk[i] = scale_pair<T>(pk[i], alpha);
+                            tc5_st16(t_s + 16 * w, pk);
+                        }
+                        raise(late, to);
+                    }
+                    // weights 2^(escale s - m): scale and maximum in one packed FMA,
+                    // sums as packed pairs in two chains
+                    const float nmu = (m_run == kNegInf) ? 0.f : -m_run;
+                    const f32x2 q2 = pack2(escale, escale), nmu2 = pack2(nmu, nmu);
+                    f32x2 l2[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float y0, y1;
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), q2, nmu2), y0, y1);
+                        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                        l2[i & 1] = add2(l2[i & 1], pack2(p0, p1));
+                        pk[i] = pack_pair<T>(p0, p1);
+                    }
                     tc5_st16(t_s + 16 * c, pk);
+                    float le, lo2;
+                    unpack2(add2(l2[0], l2[1]), le, lo2);
+                    l_tile += le + lo2;
                 }
-                float le, lo2;
-                unpack2(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), le, lo2);
-                l_run = l_run * alpha + (le + lo2);
+                tc5_st_wait();
+                l_run += l_tile;
                 if constexpr (Job::kMod) {
                     if (x == 0 && job.some_zero()) {
                         const int fv = 2 * it + 1;  // the tile's V among the ring's fills

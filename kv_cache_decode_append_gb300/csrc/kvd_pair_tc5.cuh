@@ -14,7 +14,9 @@
 //   * warps 0-3 and 4-7, the softmax warps of A and B: thread r owns row r
 //     (tensor-memory lane r): running max and sum in registers, weights P back
 //     into tensor memory as 16-bit pairs over the columns of S, O rescaled there
-//     when the max grows by more than 2^8.
+//     when the max has grown by more than 2^8.  A weight may be above 1 until
+//     then (16-bit weights round relatively, so none is the worse for it); one
+//     that would pass 2^24 (fp16: 2^15) moves the maximum at once.
 // While the softmax warps of one block work, the tensor core runs the other
 // block's products.  Tensor memory: S_A, S_B of 128 columns (P_X over the first
 // 64 of S_X), O_A, O_B of D columns: all 512 for D = 128.
@@ -800,7 +802,11 @@ __global__ void __launch_bounds__(320, 1)
                 // alone are 128 registers, and modified scores' code outgrows the
                 // instruction cache (a capped 128-token chunk 118 us unrolled, 91
                 // rolled; a prefix of 16384 keys for 128 sequences 70 and 72).
-                // Sixteen softmax warps, two threads a row: 90 and 71 us.
+                // The maximum of a tile is taken with its weights, whose exponents
+                // subtract the maximum before it: a pass of its own (taken only
+                // while some row of the warp has seen nothing) took 91 us where
+                // this takes 81; the prefix 72 and 73.  Sixteen softmax warps, two
+                // threads a row, take 80 and 72.
                 if (__any_sync(0xffffffffu, m_run == kNegInf)) {
                     float mx = kNegInf;
 #pragma unroll 1

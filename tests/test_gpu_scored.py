@@ -240,3 +240,21 @@ def test_binding_refuses():
         with pytest.raises(kvd.KvdError) as e:
             c.run(False, **bad)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("order", ["rising", "mixed"])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("f32", 64)])
+def test_maxima_that_jump(dtype, D, order):
+    """Every 32 keys a row's scores lie some 2^40 higher (or elsewhere at random): the maximum moves inside
+    tiles, far beyond what a weight may exceed it by."""
+    for N, past in ((40, [333, 77]), (1, [700, 64])):
+        c = Case(2, 4, 2, D, N, past, dtype, window=10 ** 6, seed=300)
+        steps = np.arange(-(-c.k.shape[2] // 32)) * 28.0 * (D / 64) ** 0.5
+        if order == "mixed":
+            np.random.default_rng(3).shuffle(steps)
+        u = torch.full((D,), D ** -0.5)
+        c.q = (c.q.float() / 2 + 8 * u).to(c.dt)
+        c.k = (c.k.float() + torch.from_numpy(np.repeat(steps, 32)[:c.k.shape[2]]).float()[None, None, :, None] * u).to(c.dt)
+        out, err = c.run(False)
+        assert err == 0
+        c.check(out)

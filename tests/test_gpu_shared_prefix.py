@@ -210,3 +210,22 @@ def test_binding_and_library_refuse():
         with pytest.raises(kvd.KvdError) as e:
             kvd.kvd_shared_prefix_attention(x["q"], x["kp"], x["vp"], S, x["k"], x["v"], out, past, max(c.past), workspace=w)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("order", ["rising", "mixed"])
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f16", 128), ("f32", 64)])
+def test_maxima_that_jump(dtype, D, order):
+    """Every 32 keys of the prefix a row's scores lie some 2^40 higher (or elsewhere at random): the maximum
+    moves inside tiles, far beyond what a weight may exceed it by."""
+    c = Case(5, 8, 2, D, 3, 500, [70, 0, 3, 64, 200], dtype, seed=301)
+    steps = np.arange(-(-c.kp.shape[1] // 32)) * 28.0 * (D / 64) ** 0.5
+    if order == "mixed":
+        np.random.default_rng(4).shuffle(steps)
+    u = torch.full((D,), D ** -0.5)
+    c.q = (c.q.float() / 2 + 8 * u).to(c.dt)
+    c.kp = (c.kp.float() + torch.from_numpy(np.repeat(steps, 32)[:c.kp.shape[1]]).float()[None, :, None] * u).to(c.dt)
+    # (the sequences' own keys: about where the prefix ends)
+    c.k = (c.k.float() + float(steps.max()) * u).to(c.dt)
+    out, err = c.run(False)
+    assert err == 0
+    c.check(out)

@@ -435,8 +435,8 @@ kvd_status min_occupancy(int dev, const AttnVariant &vp, const AttnVariant &vt, 
 // Modified scores, workspaces: at least this much room for the tickets.
 constexpr size_t kScoredTicketBytes = 256 * 1024;
 // The streaming kernel's CTAs: about this many for each one that is resident at
-// a time (1, 2 and 4: the long-context step 96.6 / 95.3 / 98.9 us, 16 x 12 heads
-// of 16 rows over documents 32.1 / 28.2 / 32.4), and at most this many slots
+// a time (1, 2, 3 and 4: the long-context step 96.6 / 95.3 / 96.4 / 98.9 us, 16 x 12
+// heads of 16 rows over documents 32.1 / 28.2 / 32.4 / 32.4), and at most this many slots
 // (CTAs that the longest heads would need).
 constexpr int kStreamRounds = 2;
 constexpr long long kStreamMaxSlots = 8192;
@@ -461,13 +461,18 @@ kvd_status make_stream_plan(int B, int H_kv, int D, int N, int max_past_len, kvd
     // kStreamMaxSlots for what they may see at most.
     const long long tiles = ((keys > 0 ? keys : (long long)max_past_len + N) + 63) / 64;
     const long long expect = std::min<long long>(tiles, window > 0 ? ((long long)window + N) / 64 + 3 : tiles);
-    long long per = heads * expect / ((long long)kStreamRounds * stream_ctas_per_sm(D, pl->rows) * sms);
+    const long long ctas = (long long)kStreamRounds * stream_ctas_per_sm(D, pl->rows) * sms;
+    long long per = heads * expect / ctas;
     per = std::max(per, (heads * tiles + kStreamMaxSlots - 1) / kStreamMaxSlots);
     per = std::min<long long>(std::max<long long>((per + 3) / 4 * 4, 4), std::max<long long>(tiles, 4));
     pl->sms = sms;
     pl->cta_tiles = (int)per;
     pl->grid = 0;  // (from heads and splits)
-    pl->max_splits = (int)std::max<long long>((tiles + per - 1) / per, 1);
+    // (CTAs per head: for what is expected, or enough for kStreamRounds rounds,
+    // not for all that the rows may see: of 17 per head behind a 1024-key
+    // window 14 had nothing to do: 32.6 us, 32.0 without them)
+    const long long most = std::max((expect + per - 1) / per, (ctas + heads - 1) / heads);
+    pl->max_splits = (int)std::max<long long>(std::min((tiles + per - 1) / per, most), 1);
     pl->stream_fn = dtype == KVD_BF16 ? stream_kernel_bf16(D, pl->rows, paged) : stream_kernel_f16(D, pl->rows, paged);
     pl->early = pl->merge_pass = false;
     pl->cluster = 0;

@@ -74,6 +74,7 @@ template <int D, int NR> struct StreamShape {
     // against 3 steps and 2: the long-context step 95.3 / 96.7 us, a 1024-key
     // window 32.4 / 32.6, 16 x 12 heads of 16 rows over documents 28.2 / 31.2;
     // 16 rows of D = 128 at 2 CTAs with 2 steps / 3: 17.1 / 17.9 us (53 MB).
+    // Smaller steps of D = 64 (16 keys, 3 of them) at 4 CTAs: the documents 30.6.
     static constexpr int kCtas = D == 128 && NR == 2 ? 2 : 3;
     static constexpr int kDepth = 2;
     static constexpr int kRingBytes = kDepth * 2 * kHalf;

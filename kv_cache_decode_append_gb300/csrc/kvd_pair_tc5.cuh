@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(320, 1)
     }
 }
 
-template <typename T> bool pick_prefix_tc5(int D, bool paged, PrefixVariant *v)
+template <typename T> bool pick_pair_prefix(int D, bool paged, PrefixVariant *v)
 {
     if (D != 64 && D != 128) return false;
     if (D == 64) {

@@ -2,5 +2,5 @@
 #include "kvd_pair_tc5.cuh"
 
 namespace kvd {
-bool prefix_variant_bf16(int D, bool paged, PrefixVariant *v) { return pick_prefix_tc5<__nv_bfloat16>(D, paged, v); }
+bool prefix_variant_bf16(int D, bool paged, PrefixVariant *v) { return pick_pair_prefix<__nv_bfloat16>(D, paged, v); }
 }  // namespace kvd

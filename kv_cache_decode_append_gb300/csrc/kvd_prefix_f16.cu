@@ -2,5 +2,5 @@
 #include "kvd_pair_tc5.cuh"
 
 namespace kvd {
-bool prefix_variant_f16(int D, bool paged, PrefixVariant *v) { return pick_prefix_tc5<__half>(D, paged, v); }
+bool prefix_variant_f16(int D, bool paged, PrefixVariant *v) { return pick_pair_prefix<__half>(D, paged, v); }
 }  // namespace kvd

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256, 1) prefix_simt_kernel(const PrefixArgs a)
     float *qs = reinterpret_cast<float *>(smem_simt + S::kQOff), *ks = reinterpret_cast<float *>(smem_simt + S::kKOff);
     float *vs = reinterpret_cast<float *>(smem_simt + S::kVOff), *ps = reinterpret_cast<float *>(smem_simt + S::kPOff);
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    // (no griddepcontrol.wait yet: as prefix_tc5_kernel)
+    // (no griddepcontrol.wait yet: as the tcgen05 form, PrefixJob::kWaitFirst)
     int lo, hi;
     prefix_range(a, &lo, &hi);
 
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256, 1) prefix_simt_kernel(const PrefixArgs a)
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // (as prefix_tc5_kernel)
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (as pair_tc5_kernel)
 }
 
 template <int D> void make_prefix_simt(bool paged, PrefixVariant *v)

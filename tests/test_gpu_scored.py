@@ -110,8 +110,8 @@ def _docs(past, N, at):
     return [[a if i < max(1, N // 2) else P + N // 2 for i in range(N)] for P, a in zip(past, at)]
 
 
-# rows per KV head (g N) pick the kernel: fp32 and few rows the CUDA cores,
-# 4 .. 16 mma.sync, 17 and more tcgen05
+# rows per KV head (g N) and the type pick the kernel: fp32 the CUDA cores, 16-bit
+# types the streaming kernel up to 16 rows, tcgen05 in pairs of blocks from 17 on
 CASES = {
     # plain: the same call as kvd_decode_attention
     "plain": dict(B=2, H_q=4, H_kv=2, D=64, N=1, past=[100, 0], dtype="bf16"),

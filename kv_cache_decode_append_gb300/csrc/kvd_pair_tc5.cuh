@@ -125,10 +125,24 @@ __device__ __forceinline__ void tc5_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
+// tcgen05.ld of 64 consecutive 32-bit columns of this thread's lane, waited for.
+__device__ __forceinline__ void tc5_ld(uint32_t taddr, uint32_t (&r)[64])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tc5_ld(uint32_t taddr, uint32_t (&r)[32]) { tc5_ld32(taddr, r); }
+
 // tcgen05.st of 16 consecutive 32-bit columns of this thread's lane; not waited
 // for (tc5_st_wait).
 __device__ __forceinline__ void tc5_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc5_st16(uint32_t taddr, const uint32_t (&r)[16])
+__device__ __forceinline__ void tc5_st16(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
@@ -165,6 +179,7 @@ template <typename T, int D, bool kPaged> struct PrefixJob {
     using Args = PrefixArgs;
     static constexpr bool kMod = false;
     static constexpr int kSlots = D == 128 ? 5 : 6;
+    static constexpr int kCols = 64;
     const Args &a;
     int t, lo, hi, u, k;
 
@@ -223,12 +238,12 @@ template <typename T, int D, bool kPaged> struct PrefixJob {
     }
     __device__ void begin(int, int) {}
     __device__ void tile() {}
-    __device__ __forceinline__ void scores(uint32_t (&s)[32], int c, bool) const
+    __device__ __forceinline__ void scores(uint32_t (&s)[kCols], int c, bool) const
     {
-        const int left = a.S - (k * 128 + c * 32);
-        if (left < 32) {
+        const int left = a.S - (k * 128 + c * kCols);
+        if (left < kCols) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < kCols; ++i)
                 if (i >= left) s[i] = 0xff800000u;  // -inf
         }
     }
@@ -274,6 +289,7 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
     using Args = AttnScoredArgs;
     static constexpr bool kMod = true;
     static constexpr int kSlots = D == 128 ? 4 : 6;  // (the sequences' tables take the fifth's place)
+    static constexpr int kCols = 32;
     static constexpr bool kWaitFirst = true;
     const Args &a;
     const int *pre, *pl;
@@ -538,6 +554,7 @@ __global__ void __launch_bounds__(320, 1)
     using Job = JobOf<T, D, kPaged>;
     using S = PairTc5Shape<D, Job::kSlots>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int kCols = Job::kCols;  // columns that a softmax thread takes at a time
     constexpr float kRescaleThreshold = 8.0f;
     constexpr float kLateLimit = kBf16 ? 24.0f : 15.0f;  // (fp16 weights end at 2^16)
     const float kNegInf = __int_as_float(0xff800000);
@@ -792,27 +809,28 @@ __global__ void __launch_bounds__(320, 1)
                         tc5_st32(t_o + c0, o);
                     }
                 };
-                auto chunk_max = [&](const uint32_t (&s)[32]) -> float {
+                auto chunk_max = [&](const uint32_t (&s)[kCols]) -> float {
                     float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                    for (int i = 0; i < kCols; i += 2) m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
                     return max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                 };
-                // 32 columns at a time and rolled: over the whole tile, the scores
+                // kCols columns at a time and rolled: over the whole tile, the scores
                 // alone are 128 registers, and modified scores' code outgrows the
-                // instruction cache (a capped 128-token chunk 118 us unrolled, 91
-                // rolled; a prefix of 16384 keys for 128 sequences 70 and 72).
+                // instruction cache (a capped 128-token chunk 118 us unrolled, 91 in
+                // steps of 32).  A prefix of 16384 keys for 128 sequences: 73.0 us in
+                // steps of 32, 69.2 in steps of 64 (fewer waits for tensor memory).
                 // The maximum of a tile is taken with its weights, whose exponents
                 // subtract the maximum before it: a pass of its own (taken only
                 // while some row of the warp has seen nothing) took 91 us where
-                // this takes 81; the prefix 72 and 73.  Sixteen softmax warps, two
+                // this takes 81.  Sixteen softmax warps, two
                 // threads a row, take 80 and 72.
                 if (__any_sync(0xffffffffu, m_run == kNegInf)) {
                     float mx = kNegInf;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t s[32];
-                        tc5_ld32(t_s + 32 * c, s);
+                    for (int c = 0; c < 128 / kCols; ++c) {
+                        uint32_t s[kCols];
+                        tc5_ld(t_s + kCols * c, s);
                         job.scores(s, c, job.maximum_modified());
                         mx = fmaxf(mx, chunk_max(s));
                     }
@@ -822,9 +840,9 @@ __global__ void __launch_bounds__(320, 1)
                 const float escale = job.exponent_scale();
                 float l_tile = 0.f;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {  // (weights 32 c .. over columns that are read)
-                    uint32_t s[32], pk[16];
-                    tc5_ld32(t_s + 32 * c, s);
+                for (int c = 0; c < 128 / kCols; ++c) {  // (weights over columns that are read)
+                    uint32_t s[kCols], pk[kCols / 2];
+                    tc5_ld(t_s + kCols * c, s);
                     job.scores(s, c, true);
                     const float top = chunk_max(s) * escale;
                     m_seen = fmaxf(m_seen, top);
@@ -834,11 +852,12 @@ __global__ void __launch_bounds__(320, 1)
                         const float alpha = late ? fast_exp2(m_run - to) : 1.f;
                         l_tile *= alpha;
                         tc5_st_wait();
-                        for (int w = 0; w < c; ++w) {
-                            tc5_ld16(t_s + 16 * w, pk);
+                        for (int w = 0; w < c * kCols / 32; ++w) {
+                            uint32_t pw[16];
+                            tc5_ld16(t_s + 16 * w, pw);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) pk[i] = scale_pair<T>(pk[i], alpha);
-                            tc5_st16(t_s + 16 * w, pk);
+                            for (int i = 0; i < 16; ++i) pw[i] = scale_pair<T>(pw[i], alpha);
+                            tc5_st16(t_s + 16 * w, pw);
                         }
                         raise(late, to);
                     }
@@ -848,14 +867,15 @@ __global__ void __launch_bounds__(320, 1)
                     const f32x2 q2 = pack2(escale, escale), nmu2 = pack2(nmu, nmu);
                     f32x2 l2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < kCols / 2; ++i) {
                         float y0, y1;
                         unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), q2, nmu2), y0, y1);
                         const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
                         l2[i & 1] = add2(l2[i & 1], pack2(p0, p1));
                         pk[i] = pack_pair<T>(p0, p1);
                     }
-                    tc5_st16(t_s + 16 * c, pk);
+#pragma unroll
+                    for (int w = 0; w < kCols / 2; w += 16) tc5_st16(t_s + c * (kCols / 2) + w, pk + w);
                     float le, lo2;
                     unpack2(add2(l2[0], l2[1]), le, lo2);
                     l_tile += le + lo2;

@@ -50,6 +50,8 @@
 
 namespace kvd {
 
+constexpr int kCols = 64;  // columns of S that a softmax thread takes at a time
+
 // kSlots: ring slots (a K or a V tile each).
 template <int D, int kSlots_> struct PairTc5Shape {
     static constexpr int kTK = 128;
@@ -179,7 +181,6 @@ template <typename T, int D, bool kPaged> struct PrefixJob {
     using Args = PrefixArgs;
     static constexpr bool kMod = false;
     static constexpr int kSlots = D == 128 ? 5 : 6;
-    static constexpr int kCols = 64;
     const Args &a;
     int t, lo, hi, u, k;
 
@@ -289,7 +290,6 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
     using Args = AttnScoredArgs;
     static constexpr bool kMod = true;
     static constexpr int kSlots = D == 128 ? 4 : 6;  // (the sequences' tables take the fifth's place)
-    static constexpr int kCols = 32;
     static constexpr bool kWaitFirst = true;
     const Args &a;
     const int *pre, *pl;
@@ -462,12 +462,12 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
         open = has(1) && max(key0, key1) + 64 <= k_end() && row_sees_all<64>(rs, mod.pre, key0) &&
                row_sees_all<64>(rs, mod.pre, key1);
     }
-    // Columns 32 c .. 32 c + 31 of the tile's raw scores, bounded (-inf), and
+    // The c-th kCols columns of the tile's raw scores, bounded (-inf), and
     // with `modify` modified first (to log2 units; a cap alone keeps the order of
     // scores, so a row's maximum is capped rather than its scores).
-    __device__ __forceinline__ void scores(uint32_t (&s)[32], int c, bool modify) const
+    __device__ __forceinline__ void scores(uint32_t (&s)[kCols], int c, bool modify) const
     {
-        const int half = c / 2, base = (half == 0 ? key0 : key1) + (c % 2) * 32;
+        const int half = c * kCols / 64, base = (half == 0 ? key0 : key1) + c * kCols % 64;
         if (modify) {
             if (a.cap > 0.f) {
                 const float in = a.qscale * a.cap_in;
@@ -475,7 +475,7 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
                 // (cap_score for two with one reciprocal: 1 / a and 1 / b from
                 // 1 / (a b), the exponents limited to 2^60, where tanh is 1)
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int i = 0; i < kCols; i += 2) {
                     float x0, x1;
                     unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), in2), x0, x1);
                     const f32x2 e = add2(pack2(fast_exp2(fminf(x0, 60.f)), fast_exp2(fminf(x1, 60.f))), one2);
@@ -490,14 +490,14 @@ template <typename T, int D, bool kPaged> struct ScoredJob {
             if (a.slopes != nullptr) {
                 const float d0 = (float)(rs.p - base), q = a.cap > 0.f ? 1.f : a.qscale;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)  // (whole numbers: d0 - i is exact below 2^24)
+                for (int i = 0; i < kCols; ++i)  // (whole numbers: d0 - i is exact below 2^24)
                     s[i] = __float_as_uint(fmaf(-rs.slope, fabsf(d0 - (float)i), __uint_as_float(s[i]) * q));
             }
         }
         if (!open) {
             const int end = has(half) ? k_end() : base;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < kCols; ++i)
                 if (base + i >= end || !row_sees(rs, mod.pre, base + i)) s[i] = 0xff800000u;
         }
     }
@@ -554,7 +554,6 @@ __global__ void __launch_bounds__(320, 1)
     using Job = JobOf<T, D, kPaged>;
     using S = PairTc5Shape<D, Job::kSlots>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int kCols = Job::kCols;  // columns that a softmax thread takes at a time
     constexpr float kRescaleThreshold = 8.0f;
     constexpr float kLateLimit = kBf16 ? 24.0f : 15.0f;  // (fp16 weights end at 2^16)
     const float kNegInf = __int_as_float(0xff800000);
@@ -818,13 +817,13 @@ __global__ void __launch_bounds__(320, 1)
                 // kCols columns at a time and rolled: over the whole tile, the scores
                 // alone are 128 registers, and modified scores' code outgrows the
                 // instruction cache (a capped 128-token chunk 118 us unrolled, 91 in
-                // steps of 32).  A prefix of 16384 keys for 128 sequences: 73.0 us in
-                // steps of 32, 69.2 in steps of 64 (fewer waits for tensor memory).
+                // steps of 32).  Steps of 64 against 32, which wait twice as often for
+                // tensor memory: the chunk 77 / 81 us, a prefix of 16384 keys for 128
+                // sequences 69.2 / 73.0.
                 // The maximum of a tile is taken with its weights, whose exponents
-                // subtract the maximum before it: a pass of its own (taken only
-                // while some row of the warp has seen nothing) took 91 us where
-                // this takes 81.  Sixteen softmax warps, two
-                // threads a row, take 80 and 72.
+                // subtract the maximum before it: a pass of its own (taken only while
+                // some row of the warp has seen nothing) took 91 us where this takes
+                // 81.  Sixteen softmax warps, two threads a row: 80.
                 if (__any_sync(0xffffffffu, m_run == kNegInf)) {
                     float mx = kNegInf;
 #pragma unroll 1

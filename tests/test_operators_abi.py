@@ -162,3 +162,9 @@ def test_shared_prefix_refuses_its_own_arguments(lib):
     assert _paged_prefix(lib, page_size=32) == INVALID
     assert lib.kvd_shared_prefix_workspace_bytes(1, 4, 2, 64, 1, -1, 10, BF16) == 0
     assert lib.kvd_shared_prefix_workspace_bytes(1, 3, 2, 64, 1, 10, 10, BF16) == 0
+
+
+def test_rope_append_unit_bound(lib):
+    """A token's 16-byte units: below 2^26, as their divisions assume."""
+    assert _rope(lib, H_q=(1 << 24), H_kv=1, D=64, dtype=BF16) == UNSUPPORTED  # 4 pairs of chunks a row
+    assert _rope(lib, H_q=(1 << 24), H_kv=1, D=64, dtype=BF16, B=0) == OK

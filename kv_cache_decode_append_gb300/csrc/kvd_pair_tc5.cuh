@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kJoinThreads) pair_join_kernel(const AttnScore
     PieceJoin<D> j;
     const int rows = pair_slot_rows(a), sr = k % 2 * 128 + chunk * 32 + lane;
     const float *ml = pair_ml(a, D, grid);
-    j.pieces(reinterpret_cast<const float4 *>(a.part), ml, rows, sr, c0, seg.y,
+    j.template pieces<false>(reinterpret_cast<const float4 *>(a.part), ml, rows, sr, c0, seg.y,
              [&](int i) { return (size_t)(seg.x + i) * 2 + (i == 0 ? 1 : 0); });
     j.template write<T>(static_cast<T *>(a.out) + ((size_t)bh * a.rows + rg) * D + c0 * 4);
 }

@@ -173,10 +173,7 @@ def load() -> _Lib:
 
 class _Raw:
     def __getattr__(self, name):
-        # (kept: the next look-up finds it without a call)
-        f = getattr(load(), name)
-        setattr(self, name, f)
-        return f
+        return getattr(load(), name)
 
 
 raw = _Raw()
